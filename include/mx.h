@@ -466,6 +466,149 @@ mx_status mx_grouped_gemm_quantize(const mx_tensor* A, const int32_t* d_group_of
 mx_status mx_clip_count(const void* src, int32_t src_dtype, int64_t R, int64_t C, int64_t ld_src,
                         const mx_quant_cfg* cfg, int32_t elem, uint64_t* count, void* stream);
 
+/* ------------------------------------------------------------------ feed-forward block
+ * What stands between the products of an MX feed-forward block: the gated
+ * block on MX operands, layer norm and dropout, each with its backward pass. */
+
+/* Activation of the gate projection. */
+typedef enum {
+  MX_ACT_SILU = 0,      /* g * sigmoid(alpha g)                                               */
+  MX_ACT_GELU = 1,      /* g * (1 + erf(g / sqrt 2)) / 2                                      */
+  MX_ACT_GELU_TANH = 2  /* g * (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2                  */
+} mx_act;
+
+/* Where the gate and up rows of the weight operand [2N, K] are (and, in the
+ * same order, the columns of the projections' gradient [M, 2N]). */
+typedef enum {
+  MX_GATE_INTERLEAVED = 0,  /* gate n at row 2n, up n at row 2n + 1 */
+  MX_GATE_HALVES = 1        /* gate n at row n, up n at row N + n   */
+} mx_gate_layout;
+
+/* A gated block: h = act(min(g, limit)) * (clamp(u, -limit, limit) + up_shift). */
+typedef struct {
+  int32_t act;      /* mx_act                                                  */
+  int32_t layout;   /* mx_gate_layout                                          */
+  float alpha;      /* slope of the SiLU's sigmoid (finite, > 0); 1 = plain    */
+  float limit;      /* clamp of the projections (>= 0); 0 = none               */
+  float up_shift;   /* added to the clamped up projection (finite)             */
+} mx_gate_cfg;
+
+/*
+ * mx_gemm_gated — a gated feed-forward block in one kernel: both projections
+ * of A [M, K] with the weight operand B [2N, K] (gate and up rows), the
+ * activation and the product,
+ *   g, u  the gate and up columns of P = A B^T (float32, as mx_gemm),
+ *   H[m, n] = act(min(g, limit)) * (clamp(u, -limit, limit) + up_shift),
+ * so P never reaches memory.  The formula is evaluated in float32 and rounded
+ * once to h_dtype; NaN in an operand makes its outputs NaN (a clamp keeps it).
+ *
+ *   A, B   host structs of device buffers, as mx_gemm: any element types, 1-D
+ *          or 2-D scales; B->rows = 2N must be even.
+ *   H      device; [M, N] of h_dtype, row stride ldh elements (>= N).
+ *   M or N = 0: nothing is written.  K = 0: the projections are zero.
+ * Each output's K products are summed in one float32 accumulator per part of
+ * the K range (no split over workgroups, no workspace): with n 64-deep steps
+ * the error of a projection is at most (n - 1) 2^-24 sum|a b| for MXFP4.
+ */
+mx_status mx_gemm_gated(const mx_tensor* A, const mx_tensor* B, const mx_gate_cfg* cfg, void* H, int32_t h_dtype,
+                        int64_t ldh, void* stream);
+
+/*
+ * mx_gemm_gated_backward — the backward pass of mx_gemm_gated through the
+ * product, the activation and the clamps: the gradient of the projections
+ *   dg = dH * (clamp(u) + up_shift) * act'(min(g, limit)) * [g <= limit]
+ *   du = dH * act(min(g, limit)) * [|u| <= limit]
+ * with g and u recomputed from A and B in the same kernel (nothing is saved by
+ * the forward pass).  dP holds dg and du in the column order that B has rows,
+ * so the data and weight gradients are products like any linear layer's:
+ * dA = dP B and dB = dP^T A (mx_quantize of dP along either axis, mx_gemm).
+ *
+ *   dH     device; [M, N] of dh_dtype, row stride lddh elements (>= N).
+ *   dP     device; [M, 2N] of dp_dtype, row stride lddp elements (>= 2N).
+ */
+mx_status mx_gemm_gated_backward(const mx_tensor* A, const mx_tensor* B, const mx_gate_cfg* cfg, const void* dH,
+                                 int32_t dh_dtype, int64_t lddh, void* dP, int32_t dp_dtype, int64_t lddp,
+                                 void* stream);
+
+/*
+ * mx_grouped_gemm_gated, mx_grouped_gemm_gated_backward — the same block for
+ * rows grouped by expert: rows [off[e], off[e+1]) of A, H, dH and dP belong to
+ * expert e.  Groups, offsets, expert strides and A (1-D scales) as in
+ * mx_grouped_gemm; rows past off[E] are neither read nor written.
+ */
+mx_status mx_grouped_gemm_gated(const mx_tensor* A, const int32_t* d_group_offsets, int32_t E, const mx_tensor* B,
+                                int64_t expert_stride_codes, int64_t expert_stride_scales, const mx_gate_cfg* cfg,
+                                void* H, int32_t h_dtype, int64_t ldh, void* stream);
+
+mx_status mx_grouped_gemm_gated_backward(const mx_tensor* A, const int32_t* d_group_offsets, int32_t E,
+                                         const mx_tensor* B, int64_t expert_stride_codes,
+                                         int64_t expert_stride_scales, const mx_gate_cfg* cfg, const void* dH,
+                                         int32_t dh_dtype, int64_t lddh, void* dP, int32_t dp_dtype, int64_t lddp,
+                                         void* stream);
+
+/*
+ * mx_layer_norm — y = (x - mean) * rstd * weight + bias over each row of x
+ * [R, C], mean = sum x / C, rstd = 1 / sqrt(sum (x - mean)^2 / C + eps).  The
+ * statistics and the formula are float32 (the variance from the centred
+ * values, not from a difference of sums); y is rounded once.
+ *
+ *   x, y    device; [R, C] of `dtype` (mx_dtype, one type for both), row strides
+ *           ldx, ldy elements (>= C); element-aligned.  y may be x itself.
+ *   weight  device; [C] of w_dtype; NULL = 1.  bias: likewise; NULL = 0.
+ *   eps     >= 0, finite.
+ *   mean, rstd  device; float32 [R] each, for the backward pass; NULL = not stored.
+ *   R or C = 0: nothing is written.  NaN or Inf in a row makes that row NaN.
+ */
+mx_status mx_layer_norm(const void* x, int32_t dtype, int64_t R, int64_t C, int64_t ldx, const void* weight,
+                        const void* bias, int32_t w_dtype, float eps, void* y, int64_t ldy, float* mean, float* rstd,
+                        void* stream);
+
+/*
+ * mx_layer_norm_backward — the gradients of mx_layer_norm:
+ *   xh = (x - mean) * rstd,  gy = dy * weight,
+ *   dx = rstd * (gy - sum_c(gy) / C - xh * sum_c(gy * xh) / C),
+ *   dweight[c] = sum_r dy * xh,  dbias[c] = sum_r dy,
+ * sums in float32 in an order fixed by the shape (the same bits on every run).
+ *
+ *   dy, x, dx   device; [R, C] of `dtype`, row strides lddy, ldx, lddx (>= C).
+ *               dx may be dy or x itself; NULL = not wanted.
+ *   mean, rstd  device; float32 [R] from the forward pass.
+ *   weight      device; [C] of w_dtype, NULL = 1.
+ *   dweight, dbias  device; [C] of w_dtype; NULL = not wanted.  R = 0 writes zeros.
+ *   workspace   device, 16-byte aligned, mx_layer_norm_backward_workspace_size(R, C)
+ *               bytes when dweight or dbias is wanted (else may be NULL);
+ *               contents before and after are of no meaning.
+ */
+mx_status mx_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_t R, int64_t C, int64_t lddy,
+                                 int64_t ldx, const float* mean, const float* rstd, const void* weight,
+                                 int32_t w_dtype, void* dx, int64_t lddx, void* dweight, void* dbias, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace mx_layer_norm_backward needs for an [R, C] input. */
+size_t mx_layer_norm_backward_workspace_size(int64_t R, int64_t C);
+
+/*
+ * mx_dropout — y = keep ? x * 65536 / (65536 - T) : 0 (+ residual), with
+ * T = p * 65536 rounded to nearest (ties to even) and element e = r*C + c of
+ * [R, C] kept iff its 16-bit draw is >= T: the probability of a drop is
+ * exactly T / 65536 and the mean of y is exactly x (+ residual).  The draw is
+ * the 16-bit half (e & 1) of word ((e >> 1) & 3) of Philox4x32-10 with counter
+ * (q mod 2^32, q >> 32, offset mod 2^32, offset >> 32), q = e >> 3, and key
+ * (seed mod 2^32, seed >> 32): mx_quantize's draws (use another seed or offset
+ * than a quantizer of the same step).  The mask depends on seed, offset and e
+ * alone and is never stored: the backward pass is this call on the gradient
+ * with the same p, seed and offset and no residual.  Computed in float32,
+ * rounded once.  A dropped NaN or Inf gives 0; p >= 1 - 2^-17 drops everything.
+ *
+ *   x, residual, y  device; [R, C] of `dtype`, row strides ldx, ldr, ldy
+ *                   elements (>= C); element-aligned.  residual NULL = none.
+ *                   y may be x or residual itself.
+ *   p               in [0, 1].
+ *   R or C = 0: nothing is written.
+ */
+mx_status mx_dropout(const void* x, int32_t dtype, int64_t R, int64_t C, int64_t ldx, float p, uint64_t seed,
+                     uint64_t offset, const void* residual, int64_t ldr, void* y, int64_t ldy, void* stream);
+
 /* Message describing the last failed call on this thread ("" if none). */
 const char* mx_last_error(void);
 

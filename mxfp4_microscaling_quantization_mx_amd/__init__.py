@@ -11,6 +11,14 @@ missing, every call raises: there is no fallback path.
     qt = transpose(q2d)                                 # exact, 2-D blocks only
     c = gemm(qa, qb, torch.bfloat16)                    # C = A * B^T
     c = grouped_gemm(qa, offsets, qb_stacked, torch.bfloat16)
+
+and, around the products of a feed-forward block,
+
+    h = gemm_gated(qa, qb, Gate())                      # act(gate) * up, qb = gate and up rows
+    dp = gemm_gated_backward(qa, qb, dh, Gate())        # gradient of both projections
+    y, mean, rstd = layer_norm(x, weight, bias)
+    dx, dw, db = layer_norm_backward(dy, x, mean, rstd, weight)
+    y = dropout(x, 0.1, seed=1, residual=r)
 """
 import ctypes
 import os
@@ -29,11 +37,15 @@ _ROUND = {"rne": 0, "sr": 1, "sr8": 2}
 _SCALE = {"floor": 0, "round_up": 1, "prescale_3_4": 2}
 # MX element types: name -> (mx_elem, bits per element)
 _ELEM = {"e2m1": (0, 4), "e4m3": (1, 8), "e5m2": (2, 8), "e2m3": (3, 6), "e3m2": (4, 6)}
+_ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+_GATE_LAYOUT = {"interleaved": 0, "halves": 1}
 _DTYPE = {torch.float32: MX_DT_F32, torch.bfloat16: MX_DT_BF16}
 
 EXPORTED = ("mx_quantize", "mx_quantize_gather", "mx_quantize_scatter", "mx_dequantize", "mx_transpose", "mx_gemm",
             "mx_gemm_quantize", "mx_gemm_workspace_size", "mx_gemm_noalloc", "mx_gemm_fused_quant_a", "mx_grouped_gemm",
-            "mx_grouped_gemm_quantize", "mx_clip_count",
+            "mx_grouped_gemm_quantize", "mx_clip_count", "mx_gemm_gated", "mx_gemm_gated_backward",
+            "mx_grouped_gemm_gated", "mx_grouped_gemm_gated_backward", "mx_layer_norm", "mx_layer_norm_backward",
+            "mx_layer_norm_backward_workspace_size", "mx_dropout",
             "mx_last_error", "mx_version")
 
 
@@ -49,6 +61,11 @@ class QuantCfgC(ctypes.Structure):
                 ("rounding", ctypes.c_int32), ("use_rht", ctypes.c_int32),
                 ("rht_sign_mask", ctypes.c_uint32), ("scale_mode", ctypes.c_uint32),
                 ("philox_seed", ctypes.c_uint64), ("philox_offset", ctypes.c_uint64)]
+
+
+class GateCfgC(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int32), ("layout", ctypes.c_int32), ("alpha", ctypes.c_float),
+                ("limit", ctypes.c_float), ("up_shift", ctypes.c_float)]
 
 
 class MXError(RuntimeError):
@@ -88,6 +105,20 @@ def load_library(path=LIB_PATH):
     for f in ("mx_quantize", "mx_quantize_gather", "mx_quantize_scatter", "mx_dequantize", "mx_transpose", "mx_gemm",
               "mx_gemm_quantize", "mx_gemm_noalloc", "mx_gemm_fused_quant_a", "mx_grouped_gemm",
               "mx_grouped_gemm_quantize"):
+        getattr(lib, f).restype = ctypes.c_int
+    U64, F32, PG = ctypes.c_uint64, ctypes.c_float, ctypes.POINTER(GateCfgC)
+    lib.mx_gemm_gated.argtypes = [PT, PT, PG, P, I32, I64, P]
+    lib.mx_gemm_gated_backward.argtypes = [PT, PT, PG, P, I32, I64, P, I32, I64, P]
+    lib.mx_grouped_gemm_gated.argtypes = [PT, P, I32, PT, I64, I64, PG, P, I32, I64, P]
+    lib.mx_grouped_gemm_gated_backward.argtypes = [PT, P, I32, PT, I64, I64, PG, P, I32, I64, P, I32, I64, P]
+    lib.mx_layer_norm.argtypes = [P, I32, I64, I64, I64, P, P, I32, F32, P, I64, P, P, P]
+    lib.mx_layer_norm_backward.argtypes = [P, P, I32, I64, I64, I64, I64, P, P, P, I32, P, I64, P, P, P,
+                                           ctypes.c_size_t, P]
+    lib.mx_layer_norm_backward_workspace_size.argtypes = [I64, I64]
+    lib.mx_layer_norm_backward_workspace_size.restype = ctypes.c_size_t
+    lib.mx_dropout.argtypes = [P, I32, I64, I64, I64, F32, U64, U64, P, I64, P, I64, P]
+    for f in ("mx_gemm_gated", "mx_gemm_gated_backward", "mx_grouped_gemm_gated", "mx_grouped_gemm_gated_backward",
+              "mx_layer_norm", "mx_layer_norm_backward", "mx_dropout"):
         getattr(lib, f).restype = ctypes.c_int
     lib.mx_last_error.restype = ctypes.c_char_p
     lib.mx_last_error.argtypes = []
@@ -391,6 +422,169 @@ def grouped_gemm_quantize(a, offsets, b, scale_mode="floor", out=None):
     _check(lib.mx_grouped_gemm_quantize(ctypes.byref(at), _ptr(offsets), E, ctypes.byref(b0), b.codes.stride(0),
                                         b.scales.stride(0), _SCALE[scale_mode], ctypes.byref(ot),
                                         _stream(out.codes)))
+    return out
+
+
+@dataclass(frozen=True)
+class Gate:
+    """A gated block: act(min(g, limit)) * (clamp(u, -limit, limit) + up_shift)
+    for the gate and up projections g, u (mx_gate_cfg in include/mx.h).  act:
+    "silu" (g * sigmoid(alpha g)), "gelu" or "gelu_tanh"; limit None: no
+    clamp.  layout: gate and up rows of the weight "interleaved" or in two
+    "halves" (gates first)."""
+    act: str = "silu"
+    alpha: float = 1.0
+    limit: float = None
+    up_shift: float = 0.0
+    layout: str = "interleaved"
+
+    def c_struct(self):
+        return GateCfgC(_ACT[self.act], _GATE_LAYOUT[self.layout], self.alpha,
+                        0.0 if self.limit is None else self.limit, self.up_shift)
+
+
+def _check_rows(t, shape, what):
+    if t.dim() != 2 or tuple(t.shape) != tuple(shape) or t.dtype not in _DTYPE or not t.is_cuda:
+        raise ValueError(f"{what} must be a bf16/float32 CUDA tensor of shape {tuple(shape)}")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{what} must be row-major (stride(1) == 1)")
+
+
+def _gated(what, a, b, gate, out, out_dtype, dh, offsets):
+    lib = load_library()
+    backward = dh is not None
+    if offsets is not None:
+        E, rows = b.codes.shape[0], b.codes.shape[1]
+        if offsets.dtype != torch.int32 or not offsets.is_cuda or offsets.numel() != E + 1:
+            raise ValueError("offsets must be an int32 CUDA tensor with E+1 entries")
+        bt = MxTensorC(b.codes.data_ptr(), b.scales.data_ptr(), rows, b.K, b.codes.stride(1), b.scales.stride(1),
+                       _BLOCK[b.block], _ELEM[b.elem][0])
+        group = (_ptr(offsets), E, ctypes.byref(bt), b.codes.stride(0), b.scales.stride(0))
+    else:
+        rows, bt = b.rows, b.c_struct()
+        group = (ctypes.byref(bt),)
+    N = rows // 2
+    shape = (a.rows, rows if backward else N)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=a.codes.device)
+    else:
+        _check_rows(out, shape, f"{what}: out")
+    args = ()
+    if backward:
+        _check_rows(dh, (a.rows, N), f"{what}: dh")
+        args = (_ptr(dh), _DTYPE[dh.dtype], dh.stride(0))
+    at, gc = a.c_struct(), gate.c_struct()
+    _check(getattr(lib, what)(ctypes.byref(at), *group, ctypes.byref(gc), *args, _ptr(out), _DTYPE[out.dtype],
+                              out.stride(0), _stream(out)))
+    return out
+
+
+def gemm_gated(a, b, gate=Gate(), out_dtype=torch.bfloat16, out=None):
+    """The gated feed-forward block of MX operands a [M, K] and b [2N, K]
+    (gate and up rows): both projections, the activation and the product in
+    one kernel, [M, N] (see mx_gemm_gated)."""
+    return _gated("mx_gemm_gated", a, b, gate, out, out_dtype, None, None)
+
+
+def gemm_gated_backward(a, b, dh, gate=Gate(), out_dtype=torch.bfloat16, out=None):
+    """The gradient [M, 2N] of gemm_gated's projections for the gradient dh
+    [M, N] of its output, the projections recomputed from a and b (see
+    mx_gemm_gated_backward); its columns are in the order of b's rows."""
+    return _gated("mx_gemm_gated_backward", a, b, gate, out, out_dtype, dh, None)
+
+
+def grouped_gemm_gated(a, offsets, b, gate=Gate(), out_dtype=torch.bfloat16, out=None):
+    """gemm_gated for rows grouped by expert; a, offsets and the stacked b
+    [E, 2N, K] as in grouped_gemm (see mx_grouped_gemm_gated).  Rows past
+    offsets[E] of the output are not written."""
+    return _gated("mx_grouped_gemm_gated", a, b, gate, out, out_dtype, None, offsets)
+
+
+def grouped_gemm_gated_backward(a, offsets, b, dh, gate=Gate(), out_dtype=torch.bfloat16, out=None):
+    """gemm_gated_backward for rows grouped by expert."""
+    return _gated("mx_grouped_gemm_gated_backward", a, b, gate, out, out_dtype, dh, offsets)
+
+
+def _norm_param(t, C, dtype, what):
+    if t.shape != (C,) or t.dtype not in _DTYPE or not t.is_cuda or (t.stride(0) != 1 and C > 1):
+        raise ValueError(f"{what} must be a contiguous bf16/float32 CUDA tensor of {C} entries")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must have the weight's dtype")
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None):
+    """Layer norm of the rows of a 2-D bf16/float32 CUDA tensor (see
+    mx_layer_norm): (y, mean, rstd), the row statistics in float32 for
+    layer_norm_backward."""
+    lib = load_library()
+    _check_rows(x, x.shape, "layer_norm: x")
+    R, C = x.shape
+    if weight is not None:
+        _norm_param(weight, C, None, "layer_norm: weight")
+    if bias is not None:
+        _norm_param(bias, C, None if weight is None else weight.dtype, "layer_norm: bias")
+    if out is None:
+        out = torch.empty((R, C), dtype=x.dtype, device=x.device)
+    else:
+        _check_rows(out, x.shape, "layer_norm: out")
+        if out.dtype != x.dtype:
+            raise ValueError("layer_norm: out must have x's dtype")
+    stats = torch.empty((2, R), dtype=torch.float32, device=x.device)
+    wd = weight if weight is not None else bias
+    _check(lib.mx_layer_norm(_ptr(x), _DTYPE[x.dtype], R, C, x.stride(0), _ptr(weight), _ptr(bias),
+                             MX_DT_F32 if wd is None else _DTYPE[wd.dtype], eps, _ptr(out), out.stride(0),
+                             _ptr(stats[0]), _ptr(stats[1]), _stream(x)))
+    return out, stats[0], stats[1]
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, param_dtype=None):
+    """The gradients (dx, dweight, dbias) of layer_norm (see
+    mx_layer_norm_backward).  dweight and dbias have the weight's dtype, or
+    param_dtype without one (default float32); out receives dx."""
+    lib = load_library()
+    _check_rows(x, x.shape, "layer_norm_backward: x")
+    _check_rows(dy, x.shape, "layer_norm_backward: dy")
+    if dy.dtype != x.dtype:
+        raise ValueError("layer_norm_backward: dy must have x's dtype")
+    R, C = x.shape
+    for t, n in ((mean, "mean"), (rstd, "rstd")):
+        if t.shape != (R,) or t.dtype != torch.float32 or not t.is_cuda or (t.stride(0) != 1 and R > 1):
+            raise ValueError(f"layer_norm_backward: {n} must be a contiguous float32 CUDA tensor of {R} entries")
+    if weight is not None:
+        _norm_param(weight, C, param_dtype, "layer_norm_backward: weight")
+        param_dtype = weight.dtype
+    if out is None:
+        out = torch.empty((R, C), dtype=x.dtype, device=x.device)
+    else:
+        _check_rows(out, x.shape, "layer_norm_backward: out")
+        if out.dtype != x.dtype:
+            raise ValueError("layer_norm_backward: out must have x's dtype")
+    grads = torch.empty((2, C), dtype=param_dtype or torch.float32, device=x.device)
+    nbytes = lib.mx_layer_norm_backward_workspace_size(R, C)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    _check(lib.mx_layer_norm_backward(_ptr(dy), _ptr(x), _DTYPE[x.dtype], R, C, dy.stride(0), x.stride(0), _ptr(mean),
+                                      _ptr(rstd), _ptr(weight), _DTYPE[grads.dtype], _ptr(out), out.stride(0),
+                                      _ptr(grads[0]), _ptr(grads[1]), _ptr(ws), nbytes, _stream(x)))
+    return out, grads[0], grads[1]
+
+
+def dropout(x, p, seed=0, offset=0, residual=None, out=None):
+    """Dropout of a 2-D bf16/float32 CUDA tensor from Philox draws, plus an
+    optional residual (see mx_dropout).  The backward pass is this call on the
+    gradient with the same p, seed and offset and no residual."""
+    lib = load_library()
+    _check_rows(x, x.shape, "dropout: x")
+    for t, n in ((residual, "residual"), (out, "out")):
+        if t is not None:
+            _check_rows(t, x.shape, f"dropout: {n}")
+            if t.dtype != x.dtype:
+                raise ValueError(f"dropout: {n} must have x's dtype")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    R, C = x.shape
+    _check(lib.mx_dropout(_ptr(x), _DTYPE[x.dtype], R, C, x.stride(0), p, seed & (2**64 - 1), offset & (2**64 - 1),
+                          _ptr(residual), 0 if residual is None else residual.stride(0), _ptr(out), out.stride(0),
+                          _stream(x)))
     return out
 
 

@@ -27,7 +27,8 @@ CFLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-ffp-contract=off", "-Wall", "-Wno-unused-function",
 ]
-SOURCES = ["mx_api.cpp", "quantize.hip", "dequantize.hip", "transpose.hip", "gemm.hip", "gemm_splitk.hip", "clip.hip"]
+SOURCES = ["mx_api.cpp", "quantize.hip", "dequantize.hip", "transpose.hip", "gemm.hip", "gemm_splitk.hip", "clip.hip",
+           "gated.hip", "norm.hip", "dropout.hip"]
 
 
 def _run(cmd):

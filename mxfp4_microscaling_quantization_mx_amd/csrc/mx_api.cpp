@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -650,6 +651,272 @@ mx_status mx_grouped_gemm(const mx_tensor* A, const int32_t* d_group_offsets, in
       !(tile_offsets_fit(A, ldc * (a.out_bf16 ? 2 : 4)) && tile_offsets_fit(B, 0)))
     return fail(MX_ERR_UNSUPPORTED, "mx_grouped_gemm: row strides too large for the MXFP8/MXFP6 kernels");
   return hip_status(mx::launch_grouped_gemm(a, static_cast<hipStream_t>(stream)), "mx_grouped_gemm");
+}
+
+
+// ---------------------------------------------------------------- feed-forward block
+namespace {
+
+bool known_dtype(int32_t d) { return d == MX_DT_F32 || d == MX_DT_BF16; }
+uintptr_t dtype_size(int32_t d) { return d == MX_DT_BF16 ? 2 : 4; }
+
+// A row-major [R, C] buffer of `dtype` elements, element-aligned.
+mx_status check_rows(const void* p, int32_t dtype, int64_t C, int64_t ld, const char* what, const char* name) {
+  if (!p) return fail(MX_ERR_INVALID_ARG, "%s: null %s", what, name);
+  if (ld < C)
+    return fail(MX_ERR_INVALID_ARG, "%s: row stride of %s %lld < %lld", what, name, (long long)ld, (long long)C);
+  if (!aligned(p, dtype_size(dtype)))
+    return fail(MX_ERR_INVALID_ARG, "%s: %s must be aligned to its element size", what, name);
+  return MX_OK;
+}
+
+// Validate a gated block's operands and configuration and describe them; the
+// buffers follow.  M = 0 or N = 0 leaves a.M or a.N 0.
+mx_status gated_args(const mx_tensor* A, const mx_tensor* B, const mx_gate_cfg* cfg, const char* what,
+                     mx::GatedArgs& a) {
+  char name[64];
+  std::snprintf(name, sizeof(name), "%s: A", what);
+  mx_status st = check_tensor(A, name);
+  if (st != MX_OK) return st;
+  std::snprintf(name, sizeof(name), "%s: B", what);
+  st = check_tensor(B, name);
+  if (st != MX_OK) return st;
+  if (A->K != B->K)
+    return fail(MX_ERR_INVALID_ARG, "%s: A.K=%lld != B.K=%lld", what, (long long)A->K, (long long)B->K);
+  if (B->rows % 2)
+    return fail(MX_ERR_INVALID_ARG, "%s: B holds gate and up rows, an even number (got %lld)", what,
+                (long long)B->rows);
+  if (!cfg) return fail(MX_ERR_INVALID_ARG, "%s: null gate configuration", what);
+  if (cfg->act < MX_ACT_SILU || cfg->act > MX_ACT_GELU_TANH)
+    return fail(MX_ERR_INVALID_ARG, "%s: unknown activation %d", what, cfg->act);
+  if (cfg->layout != MX_GATE_INTERLEAVED && cfg->layout != MX_GATE_HALVES)
+    return fail(MX_ERR_INVALID_ARG, "%s: unknown gate layout %d", what, cfg->layout);
+  if (!(cfg->alpha > 0.0f) || !std::isfinite(cfg->alpha))
+    return fail(MX_ERR_INVALID_ARG, "%s: alpha must be finite and > 0", what);
+  if (!(cfg->limit >= 0.0f)) return fail(MX_ERR_INVALID_ARG, "%s: limit must be >= 0 (0: none)", what);
+  if (!std::isfinite(cfg->up_shift)) return fail(MX_ERR_INVALID_ARG, "%s: up_shift must be finite", what);
+  if (A->rows > 0x7FFFFFFF || B->rows > 0x7FFFFFFF || A->K > 0x7FFFFFFF)
+    return fail(MX_ERR_UNSUPPORTED, "%s: at most 2^31 - 1 rows and K elements", what);
+  a = mx::GatedArgs{};
+  a.A = operand(A);
+  a.B = operand(B);
+  a.a_2d = A->block == MX_BLOCK_2D;
+  a.b_2d = B->block == MX_BLOCK_2D;
+  a.a_elem = A->elem;
+  a.b_elem = B->elem;
+  a.M = A->rows;
+  a.N = B->rows / 2;
+  a.K = A->K;
+  a.act = cfg->act;
+  a.halves = cfg->layout == MX_GATE_HALVES;
+  a.alpha = cfg->alpha;
+  a.limit = cfg->limit == 0.0f ? INFINITY : cfg->limit;
+  a.up_shift = cfg->up_shift;
+  return MX_OK;
+}
+
+// The output of the forward pass (dH null) or the backward pass's two buffers.
+mx_status gated_buffers(mx::GatedArgs& a, bool backward, const void* dH, int32_t dh_dtype, int64_t lddh, void* out,
+                        int32_t out_dtype, int64_t ldo, const char* what) {
+  if (!known_dtype(out_dtype)) return fail(MX_ERR_INVALID_ARG, "%s: unknown output dtype %d", what, out_dtype);
+  if (backward && !known_dtype(dh_dtype)) return fail(MX_ERR_INVALID_ARG, "%s: unknown dH dtype %d", what, dh_dtype);
+  if (a.M == 0 || a.N == 0) return MX_OK;
+  mx_status st = check_rows(out, out_dtype, backward ? 2 * a.N : a.N, ldo, what, backward ? "dP" : "H");
+  if (st != MX_OK) return st;
+  a.out = out;
+  a.ldo = ldo;
+  a.out_bf16 = out_dtype == MX_DT_BF16;
+  if (backward) {
+    st = check_rows(dH, dh_dtype, a.N, lddh, what, "dH");
+    if (st != MX_OK) return st;
+    a.dH = dH;
+    a.lddh = lddh;
+    a.dh_bf16 = dh_dtype == MX_DT_BF16;
+  }
+  return MX_OK;
+}
+
+mx_status gated_groups(mx::GatedArgs& a, const mx_tensor* A, const int32_t* offsets, int32_t E, int64_t stride_codes,
+                       int64_t stride_scales, const char* what) {
+  if (A->block != MX_BLOCK_1D)
+    return fail(MX_ERR_UNSUPPORTED, "%s: A must use 1-D blocks (expert boundaries are arbitrary rows)", what);
+  if (E < 1) return fail(MX_ERR_INVALID_ARG, "%s: E=%d < 1", what, E);
+  if (!offsets || !aligned(offsets, 4)) return fail(MX_ERR_INVALID_ARG, "%s: null or unaligned group offsets", what);
+  if (stride_codes < 0 || stride_scales < 0 || stride_codes % 16)
+    return fail(MX_ERR_INVALID_ARG, "%s: expert strides must be >= 0 (codes stride %% 16 == 0)", what);
+  a.offsets = offsets;
+  a.E = E;
+  a.stride_codes = stride_codes;
+  a.stride_scales = stride_scales;
+  return MX_OK;
+}
+
+}  // namespace
+
+mx_status mx_gemm_gated(const mx_tensor* A, const mx_tensor* B, const mx_gate_cfg* cfg, void* H, int32_t h_dtype,
+                        int64_t ldh, void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_gemm_gated";
+  mx::GatedArgs a;
+  mx_status st = gated_args(A, B, cfg, what, a);
+  if (st == MX_OK) st = gated_buffers(a, false, nullptr, 0, 0, H, h_dtype, ldh, what);
+  if (st != MX_OK) return st;
+  return hip_status(mx::launch_gated(a, static_cast<hipStream_t>(stream)), what);
+}
+
+mx_status mx_gemm_gated_backward(const mx_tensor* A, const mx_tensor* B, const mx_gate_cfg* cfg, const void* dH,
+                                 int32_t dh_dtype, int64_t lddh, void* dP, int32_t dp_dtype, int64_t lddp,
+                                 void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_gemm_gated_backward";
+  mx::GatedArgs a;
+  mx_status st = gated_args(A, B, cfg, what, a);
+  if (st == MX_OK) st = gated_buffers(a, true, dH, dh_dtype, lddh, dP, dp_dtype, lddp, what);
+  if (st != MX_OK) return st;
+  return hip_status(mx::launch_gated(a, static_cast<hipStream_t>(stream)), what);
+}
+
+mx_status mx_grouped_gemm_gated(const mx_tensor* A, const int32_t* d_group_offsets, int32_t E, const mx_tensor* B,
+                                int64_t expert_stride_codes, int64_t expert_stride_scales, const mx_gate_cfg* cfg,
+                                void* H, int32_t h_dtype, int64_t ldh, void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_grouped_gemm_gated";
+  mx::GatedArgs a;
+  mx_status st = gated_args(A, B, cfg, what, a);
+  if (st == MX_OK) st = gated_groups(a, A, d_group_offsets, E, expert_stride_codes, expert_stride_scales, what);
+  if (st == MX_OK) st = gated_buffers(a, false, nullptr, 0, 0, H, h_dtype, ldh, what);
+  if (st != MX_OK) return st;
+  return hip_status(mx::launch_gated(a, static_cast<hipStream_t>(stream)), what);
+}
+
+mx_status mx_grouped_gemm_gated_backward(const mx_tensor* A, const int32_t* d_group_offsets, int32_t E,
+                                         const mx_tensor* B, int64_t expert_stride_codes,
+                                         int64_t expert_stride_scales, const mx_gate_cfg* cfg, const void* dH,
+                                         int32_t dh_dtype, int64_t lddh, void* dP, int32_t dp_dtype, int64_t lddp,
+                                         void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_grouped_gemm_gated_backward";
+  mx::GatedArgs a;
+  mx_status st = gated_args(A, B, cfg, what, a);
+  if (st == MX_OK) st = gated_groups(a, A, d_group_offsets, E, expert_stride_codes, expert_stride_scales, what);
+  if (st == MX_OK) st = gated_buffers(a, true, dH, dh_dtype, lddh, dP, dp_dtype, lddp, what);
+  if (st != MX_OK) return st;
+  return hip_status(mx::launch_gated(a, static_cast<hipStream_t>(stream)), what);
+}
+
+mx_status mx_layer_norm(const void* x, int32_t dtype, int64_t R, int64_t C, int64_t ldx, const void* weight,
+                        const void* bias, int32_t w_dtype, float eps, void* y, int64_t ldy, float* mean, float* rstd,
+                        void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_layer_norm";
+  if (!known_dtype(dtype)) return fail(MX_ERR_INVALID_ARG, "%s: unknown dtype %d", what, dtype);
+  if (!known_dtype(w_dtype)) return fail(MX_ERR_INVALID_ARG, "%s: unknown weight dtype %d", what, w_dtype);
+  if (R < 0 || C < 0) return fail(MX_ERR_INVALID_ARG, "%s: negative shape", what);
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(MX_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", what);
+  if (R == 0 || C == 0) return MX_OK;
+  mx_status st = check_rows(x, dtype, C, ldx, what, "x");
+  if (st == MX_OK) st = check_rows(y, dtype, C, ldy, what, "y");
+  if (st != MX_OK) return st;
+  if (!aligned(weight, dtype_size(w_dtype)) || !aligned(bias, dtype_size(w_dtype)))
+    return fail(MX_ERR_INVALID_ARG, "%s: weight and bias must be aligned to their element size", what);
+  if (!aligned(mean, 4) || !aligned(rstd, 4))
+    return fail(MX_ERR_INVALID_ARG, "%s: mean and rstd must be 4-byte aligned", what);
+  mx::NormArgs a{};
+  a.x = x;
+  a.R = R;
+  a.C = C;
+  a.ldx = ldx;
+  a.bf16 = dtype == MX_DT_BF16;
+  a.weight = weight;
+  a.bias = bias;
+  a.w_bf16 = w_dtype == MX_DT_BF16;
+  a.eps = eps;
+  a.y = y;
+  a.ldy = ldy;
+  a.mean = mean;
+  a.rstd = rstd;
+  return hip_status(mx::launch_layer_norm(a, static_cast<hipStream_t>(stream)), what);
+}
+
+size_t mx_layer_norm_backward_workspace_size(int64_t R, int64_t C) {
+  if (R <= 0 || C <= 0) return 0;
+  return mx::norm_backward_workspace(R, C);
+}
+
+mx_status mx_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_t R, int64_t C, int64_t lddy,
+                                 int64_t ldx, const float* mean, const float* rstd, const void* weight,
+                                 int32_t w_dtype, void* dx, int64_t lddx, void* dweight, void* dbias, void* workspace,
+                                 size_t ws_bytes, void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_layer_norm_backward";
+  if (!known_dtype(dtype)) return fail(MX_ERR_INVALID_ARG, "%s: unknown dtype %d", what, dtype);
+  if (!known_dtype(w_dtype)) return fail(MX_ERR_INVALID_ARG, "%s: unknown weight dtype %d", what, w_dtype);
+  if (R < 0 || C < 0) return fail(MX_ERR_INVALID_ARG, "%s: negative shape", what);
+  if (C == 0) return MX_OK;
+  const uintptr_t ws = dtype_size(w_dtype);
+  if (!aligned(weight, ws) || !aligned(dweight, ws) || !aligned(dbias, ws))
+    return fail(MX_ERR_INVALID_ARG, "%s: weight, dweight and dbias must be aligned to their element size", what);
+  if (R > 0) {
+    mx_status st = check_rows(dy, dtype, C, lddy, what, "dy");
+    if (st == MX_OK) st = check_rows(x, dtype, C, ldx, what, "x");
+    if (st == MX_OK && dx) st = check_rows(dx, dtype, C, lddx, what, "dx");
+    if (st != MX_OK) return st;
+    if (!mean || !rstd || !aligned(mean, 4) || !aligned(rstd, 4))
+      return fail(MX_ERR_INVALID_ARG, "%s: null or unaligned mean or rstd", what);
+    if (dweight || dbias) {
+      const size_t need = mx::norm_backward_workspace(R, C);
+      if (!workspace || ws_bytes < need || !aligned(workspace, 16))
+        return fail(MX_ERR_INVALID_ARG,
+                    "%s: dweight and dbias need a 16-byte aligned workspace of %zu bytes (got %zu bytes at %p)", what,
+                    need, ws_bytes, workspace);
+    }
+  }
+  mx::NormBwdArgs a{};
+  a.dy = dy;
+  a.x = x;
+  a.R = R;
+  a.C = C;
+  a.lddy = lddy;
+  a.ldx = ldx;
+  a.bf16 = dtype == MX_DT_BF16;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.weight = weight;
+  a.w_bf16 = w_dtype == MX_DT_BF16;
+  a.dx = dx;
+  a.lddx = lddx;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.workspace = static_cast<float*>(workspace);
+  return hip_status(mx::launch_layer_norm_backward(a, static_cast<hipStream_t>(stream)), what);
+}
+
+mx_status mx_dropout(const void* x, int32_t dtype, int64_t R, int64_t C, int64_t ldx, float p, uint64_t seed,
+                     uint64_t offset, const void* residual, int64_t ldr, void* y, int64_t ldy, void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_dropout";
+  if (!known_dtype(dtype)) return fail(MX_ERR_INVALID_ARG, "%s: unknown dtype %d", what, dtype);
+  if (R < 0 || C < 0) return fail(MX_ERR_INVALID_ARG, "%s: negative shape", what);
+  if (!(p >= 0.0f && p <= 1.0f)) return fail(MX_ERR_INVALID_ARG, "%s: p must be in [0, 1]", what);
+  if (R == 0 || C == 0) return MX_OK;
+  mx_status st = check_rows(x, dtype, C, ldx, what, "x");
+  if (st == MX_OK) st = check_rows(y, dtype, C, ldy, what, "y");
+  if (st == MX_OK && residual) st = check_rows(residual, dtype, C, ldr, what, "residual");
+  if (st != MX_OK) return st;
+  mx::DropoutArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.y = y;
+  a.R = R;
+  a.C = C;
+  a.ldx = ldx;
+  a.ldr = ldr;
+  a.ldy = ldy;
+  a.bf16 = dtype == MX_DT_BF16;
+  a.threshold = (uint32_t)std::nearbyint((double)p * 65536.0);
+  a.seed = seed;
+  a.offset = offset;
+  return hip_status(mx::launch_dropout(a, static_cast<hipStream_t>(stream)), what);
 }
 
 }  // extern "C"

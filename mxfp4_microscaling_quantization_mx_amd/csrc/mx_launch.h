@@ -166,4 +166,72 @@ hipError_t launch_grouped_gemm(const GroupedGemmArgs& a, hipStream_t st);
 bool grouped_quantize_supported(const GroupedQuantArgs& a);
 hipError_t launch_grouped_gemm_quantize(const GroupedQuantArgs& a, hipStream_t st);
 
+// ---------------------------------------------------------------- feed-forward block
+struct NormArgs {
+  const void* x;
+  int64_t R, C, ldx;
+  bool bf16;                  // x and y (else float32)
+  const void* weight;         // nullable
+  const void* bias;           // nullable
+  bool w_bf16;
+  float eps;
+  void* y;
+  int64_t ldy;
+  float* mean;                // nullable
+  float* rstd;
+};
+
+struct NormBwdArgs {
+  const void* dy;
+  const void* x;
+  int64_t R, C, lddy, ldx;
+  bool bf16;
+  const float* mean;
+  const float* rstd;
+  const void* weight;         // nullable
+  bool w_bf16;
+  void* dx;                   // nullable
+  int64_t lddx;
+  void* dweight;              // nullable
+  void* dbias;                // nullable
+  float* workspace;           // norm_backward_workspace bytes when dweight or dbias
+};
+
+struct DropoutArgs {
+  const void* x;
+  const void* residual;       // nullable
+  void* y;
+  int64_t R, C, ldx, ldr, ldy;
+  bool bf16;
+  uint32_t threshold;         // 0 .. 65536: dropped iff the draw is below
+  uint64_t seed, offset;
+};
+
+// The gated block of an MX product (H), or with dH its projections' gradient
+// (dP).  N counts hidden columns: B has 2N rows.  Dense: offsets null, rows
+// [0, M).  Grouped: M is the row capacity, B expert 0.
+struct GatedArgs {
+  MxOperand A, B;
+  bool a_2d, b_2d;
+  int a_elem, b_elem;
+  int64_t M, N, K;
+  int act, halves;
+  float alpha, limit, up_shift;   // limit +inf: no clamp
+  const void* dH;             // null: forward
+  int64_t lddh;
+  bool dh_bf16;
+  void* out;                  // H [M, N] or dP [M, 2N]
+  int64_t ldo;
+  bool out_bf16;
+  const int32_t* offsets = nullptr;   // device, E+1
+  int32_t E = 0;
+  int64_t stride_codes = 0, stride_scales = 0;
+};
+
+hipError_t launch_layer_norm(const NormArgs& a, hipStream_t st);
+size_t norm_backward_workspace(int64_t R, int64_t C);
+hipError_t launch_layer_norm_backward(const NormBwdArgs& a, hipStream_t st);
+hipError_t launch_dropout(const DropoutArgs& a, hipStream_t st);
+hipError_t launch_gated(const GatedArgs& a, hipStream_t st);
+
 }  // namespace mx
