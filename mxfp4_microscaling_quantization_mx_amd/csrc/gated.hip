@@ -160,13 +160,13 @@ __global__ __launch_bounds__(64 * DW) void k_gated_direct(GatedArgs a, int64_t t
       g = g + red[i][row][col];
       u = u + red[i][row][col + 16];
     }
-    const GateP p{a.act, a.halves, a.alpha, a.limit, a.up_shift};
+    const GateP p{a.act, a.alpha, a.limit, a.up_shift};
     const int64_t orow = row0 + row, c = n0 + col;
     if (!a.dH) {
-      store_out(a.out, a.out_bf16, orow * a.ldo + c, gate_forward(p, g, u));
+      store_out(a.out, a.out_bf16, orow * a.ldo + c, gate_forward_any(p, g, u));
     } else {
       float dg, du;
-      gate_backward(p, g, u, load_out(a.dH, a.dh_bf16, orow * a.lddh + c), dg, du);
+      gate_backward_any(p, g, u, load_out(a.dH, a.dh_bf16, orow * a.lddh + c), dg, du);
       store_out(a.out, a.out_bf16, orow * a.ldo + (a.halves ? c : 2 * c), dg);
       store_out(a.out, a.out_bf16, orow * a.ldo + (a.halves ? a.N + c : 2 * c + 1), du);
     }
@@ -205,6 +205,7 @@ hipError_t launch_direct_b(const GatedArgs& a, hipStream_t st) {
 
 hipError_t launch_gated(const GatedArgs& a, hipStream_t st) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
+  if (a.M >= 256 && a.N >= 128 && gated256_layout_ok(a)) return launch_gated256(a, st);
   switch (a.a_elem) {
     case 1: return launch_direct_b<1>(a, st);
     case 2: return launch_direct_b<2>(a, st);

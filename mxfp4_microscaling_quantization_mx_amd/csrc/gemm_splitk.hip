@@ -124,6 +124,7 @@ __device__ __forceinline__ SkParams load_sk(const SkParams* p) {
 
 struct SplitSched {
   static constexpr bool UNITS = true;
+  static constexpr int BMAP = t256c::B_ROWS;
   struct Seg {
     int t, S, k, slot;   // tile, its segment count, this unit's segment index, its partial slot
     int w0, slot0;       // the worker of segment 0 and that segment's slot

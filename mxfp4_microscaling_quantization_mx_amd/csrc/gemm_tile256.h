@@ -58,6 +58,7 @@
 #error "define MX_T256_NS and MX_T256_SWAP before including gemm_tile256.h"
 #endif
 
+#include "gate_device.h"
 #include "mx_device.h"
 #include "mx_launch.h"
 
@@ -84,6 +85,57 @@ struct TileInfo {
 struct Strides {
   int lda, ldsa, ldb, ldsb;
 };
+
+// Rows of the B operand behind a tile's 256 LDS rows (Sched::BMAP).
+//   B_ROWS         the 256 rows from n0.
+//   B_INTERLEAVED, B_HALVES  a gated block's weight: n0 and N count hidden
+//     columns, a tile covers 128 of them, and LDS row r holds the gate (bit 6
+//     of r clear) or up (set) row of column n0 + 64 (r / 128) + r % 64.  Each
+//     wave's four MFMA column tiles are then gates, gates, ups, ups of its 64
+//     columns, so both projections of an output sit in one lane.
+constexpr int B_ROWS = 0, B_INTERLEAVED = 1, B_HALVES = 2;
+
+// Row of B for LDS row r of the tile at n0 (limit N), or -1 past the end.
+template <int BMAP>
+__device__ __forceinline__ int b_row(int n0, int N, int r) {
+  if constexpr (BMAP == B_ROWS) return n0 + r < N ? n0 + r : -1;
+  const int c = n0 + ((r >> 7) << 6) + (r & 63), up = (r >> 6) & 1;
+  if (c >= N) return -1;
+  return BMAP == B_HALVES ? up * N + c : 2 * c + up;
+}
+
+// Destination of the gated epilogue: H [M, N], or (dH set) the gradient dP
+// [M, 2N] of the projections, with the columns in the order of B's rows.
+struct alignas(16) GateOut {
+  GateP p;
+  void* out;
+  const void* dH;
+  int ldo, lddh;
+  int out_bf16, dh_bf16;
+};
+static_assert(sizeof(GateOut) == 48, "three 16-byte LDS reads");
+
+// A wave-uniform GateOut kept in LDS, read with one wait (in scalar registers
+// across the pipeline it would spill).
+__device__ __forceinline__ GateOut load_gate_out(const GateOut* p) {
+  typedef int v4 __attribute__((ext_vector_type(4)));
+  v4 q[3];
+  const uint32_t a = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+  asm volatile(
+      "ds_read_b128 %0, %3\n\t"
+      "ds_read_b128 %1, %3 offset:16\n\t"
+      "ds_read_b128 %2, %3 offset:32\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(q[0]), "=&v"(q[1]), "=&v"(q[2])
+      : "v"(a)
+      : "memory");
+  int w[12];
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[4 * i + k] = __builtin_amdgcn_readfirstlane(q[i][k]);
+  return __builtin_bit_cast(GateOut, w);
+}
 
 // Tile order: groups of GM M-tiles, each walked N-tile by N-tile, so that a
 // run of consecutive tiles shares a few A and B panels.
@@ -156,6 +208,7 @@ __device__ __forceinline__ int load_chunk(int wave, int lane, int t) {
   return swz(8 * (wave * 4 + t) + (lane >> 3), lane & 7);
 }
 
+template <int BMAP>
 __device__ __forceinline__ void code_offsets(const TileInfo& ti, const Strides& sd, int wave, int lane, uint32_t va[4],
                                              uint32_t vb[4]) {
 #pragma unroll
@@ -163,30 +216,32 @@ __device__ __forceinline__ void code_offsets(const TileInfo& ti, const Strides& 
     const int row = 8 * (wave * 4 + t) + (lane >> 3);
     const int c = load_chunk(wave, lane, t);
     va[t] = (ti.m0 + row < ti.M) ? (uint32_t)(ti.m0 + row) * (uint32_t)sd.lda + 16u * c : OOB;
-    vb[t] = (ti.n0 + row < ti.N) ? (uint32_t)(ti.n0 + row) * (uint32_t)sd.ldb + 16u * c : OOB;
+    const int rb = t256c::b_row<BMAP>(ti.n0, ti.N, row);
+    vb[t] = rb >= 0 ? (uint32_t)rb * (uint32_t)sd.ldb + 16u * c : OOB;
   }
 }
 
 // This lane's scale-row offset for the scale loads of a tile (A rows for
 // waves 0-3, B rows for 4-7), past the end for rows past the limits.
-template <bool A2D, bool B2D>
+template <bool A2D, bool B2D, int BMAP>
 __device__ __forceinline__ uint32_t scale_offset(const TileInfo& ti, const Strides& sd, int wave, int lane) {
   const int r = 64 * (wave & 3) + lane;
   if (wave < 4) {
     const int ra = ti.m0 + r;
     return ra < ti.M ? (uint32_t)(A2D ? (ra >> 5) : ra) * (uint32_t)sd.ldsa : OOB;
   }
-  const int rb = ti.n0 + r;
-  return rb < ti.N ? (uint32_t)(B2D ? (rb >> 5) : rb) * (uint32_t)sd.ldsb : OOB;
+  const int rb = t256c::b_row<BMAP>(ti.n0, ti.N, r);
+  return rb >= 0 ? (uint32_t)(B2D ? (rb >> 5) : rb) * (uint32_t)sd.ldsb : OOB;
 }
 
-template <bool A2D, bool B2D>
+template <bool A2D, bool B2D, int BMAP>
 __device__ __forceinline__ void tile_rsrc(const TileInfo& ti, const Strides& sd, int wave, __amdgpu_buffer_rsrc_t& ra,
                                           __amdgpu_buffer_rsrc_t& rb, __amdgpu_buffer_rsrc_t& rs) {
   ra = rsrc(ti.a_codes, (uint32_t)(ti.M * sd.lda));
-  rb = rsrc(ti.b_codes, (uint32_t)(ti.N * sd.ldb));
+  const int brows = BMAP == t256c::B_ROWS ? ti.N : 2 * ti.N;
+  rb = rsrc(ti.b_codes, (uint32_t)(brows * sd.ldb));
   rs = wave < 4 ? rsrc(ti.a_scales, (uint32_t)((A2D ? ti.M / 32 : ti.M) * sd.ldsa))
-                : rsrc(ti.b_scales, (uint32_t)((B2D ? ti.N / 32 : ti.N) * sd.ldsb));
+                : rsrc(ti.b_scales, (uint32_t)((B2D ? brows / 32 : brows) * sd.ldsb));
 }
 
 // Issue the scale loads of stages 2q and 2q+1 of a tile into `sslot`: 16
@@ -517,11 +572,16 @@ __device__ __forceinline__ void store_tile(const Acc& acc, void* C, int ldc, int
 template <bool OUT_BF16, class Sched>
 __device__ __forceinline__ void store_unit(Acc& acc, const Sched& sc, int j, void* C, int64_t ldc);
 
-// Output kinds of run_tiles: float32, bf16, or the quantizing epilogue
-// (MX_T256_SWAP = 1 only).
-constexpr int OUT_F32 = 0, OUT_BF16_ = 1, OUT_MX = 2;
+// Output kinds of run_tiles: float32, bf16, the quantizing epilogue
+// (MX_T256_SWAP = 1 only), or the gated block's epilogues (forward, backward;
+// MX_T256_SWAP = 0 and a gated Sched::BMAP).
+constexpr int OUT_F32 = 0, OUT_BF16_ = 1, OUT_MX = 2, OUT_GATE = 3, OUT_GATE_BWD = 4;
 
 __device__ __forceinline__ void store_tile_mx(const Acc& acc, const QOut& q, int m0, int n0, int mlim, int nlim);
+
+template <bool BWD, int BMAP>
+__device__ __forceinline__ void store_tile_gate(const Acc& acc, const t256c::GateOut& q, int64_t row0, int n0, int mlim,
+                                                int nlim);
 
 // Run this workgroup's tiles: C tile = A[m0:m0+256] * B[n0:n0+256]^T over all
 // K for each tile sc.tile(j), j < sc.count().  The stage sequence g = j * nst
@@ -540,7 +600,10 @@ __device__ __forceinline__ void store_tile_mx(const Acc& acc, const QOut& q, int
 // store_unit (the split-K epilogue) instead of a plain store.
 template <bool A2D, bool B2D, int OUT, bool SPLIT, class Sched>
 __device__ __forceinline__ void run_tiles(const Sched& sc, const Strides& sd, int K, void* C, int64_t ldc,
-                                          uint8_t* lds, const QOut& qo = QOut{}) {
+                                          uint8_t* lds, const QOut& qo = QOut{},
+                                          const t256c::GateOut* go = nullptr) {
+  constexpr int BMAP = Sched::BMAP;
+  static_assert((OUT >= OUT_GATE) == (BMAP != t256c::B_ROWS), "the gated epilogues need the gated row order");
   static_assert((OUT == OUT_MX) == (MX_T256_SWAP != 0), "the quantizing epilogue needs the swapped operand order");
   constexpr bool UNITS = Sched::UNITS;
   static_assert(!UNITS || OUT != OUT_MX, "units end in the split-K epilogue, which stores float32 or bf16");
@@ -555,6 +618,8 @@ __device__ __forceinline__ void run_tiles(const Sched& sc, const Strides& sd, in
   auto store = [&](const TileInfo& ti) {
     if constexpr (OUT == OUT_MX)
       store_tile_mx(acc, qo, (int)ti.c_row0, ti.n0, ti.M - ti.m0, ti.N - ti.n0);
+    else if constexpr (OUT >= OUT_GATE)
+      store_tile_gate<OUT == OUT_GATE_BWD, BMAP>(acc, t256c::load_gate_out(go), ti.c_row0, ti.n0, ti.M - ti.m0, ti.N - ti.n0);
     else
       store_tile<OUT == OUT_BF16_>(acc, static_cast<uint8_t*>(C) + (ti.c_row0 * ldc + ti.n0) * ES, (int)ldc,
                                    ti.M - ti.m0, ti.N - ti.n0);
@@ -603,9 +668,9 @@ __device__ __forceinline__ void run_tiles(const Sched& sc, const Strides& sd, in
   __amdgpu_buffer_rsrc_t ra2, rb2, rs2;
   uint32_t pa[4], pb[4], psc;
   auto load_tile = [&]() {
-    tile_rsrc<A2D, B2D>(t2, sd, wave, ra2, rb2, rs2);
-    code_offsets(t2, sd, wave, lane, pa, pb);
-    psc = scale_offset<A2D, B2D>(t2, sd, wave, lane);
+    tile_rsrc<A2D, B2D, BMAP>(t2, sd, wave, ra2, rb2, rs2);
+    code_offsets<BMAP>(t2, sd, wave, lane, pa, pb);
+    psc = scale_offset<A2D, B2D, BMAP>(t2, sd, wave, lane);
   };
   auto advance = [&]() {
     if (++s2 == ns2) {
@@ -831,38 +896,42 @@ __device__ __forceinline__ void store_bf16_rows(float x0, float x1, __amdgpu_buf
   __builtin_amdgcn_raw_buffer_store_b32(__builtin_amdgcn_perm(q, p, sel), r, voff, soff, 0);
 }
 
-__device__ __forceinline__ void store_tile_bf16_lines(const Acc& acc, __amdgpu_buffer_rsrc_t r, int ldc, int nlim) {
-  static_assert(TJ % 2 == 0, "tiles are paired along N");
+// Two MFMA tiles side by side: x0, x1 hold row tile i of the wave's columns
+// 0 .. 31 and 32 .. 63 from column c0 of the workgroup's tile.
+__device__ __forceinline__ void store_lines(const v16f& x0, const v16f& x1, int i, int c0, __amdgpu_buffer_rsrc_t r,
+                                            int ldc, int nlim) {
   const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = threadIdx.x >> 7;
   const int odd = lane & 1;
   // even lane: bytes 0-1 of its own pair, then bytes 0-1 of its neighbour's;
   // odd lane: bytes 2-3 of the neighbour's, then its own bytes 2-3
   const uint32_t sel = odd ? 0x03020706u : 0x05040100u;
+  const int col = c0 + (lane & ~1);
+  const uint32_t voff = col < nlim ? (uint32_t)(((wm * TI * 32 + odd) * ldc + col) * 2) : OOB;
 #pragma unroll
-  for (int jp = 0; jp < TJ; jp += 2) {
-    const int col = wn * TJ * 32 + 32 * jp + (lane & ~1);
-    const uint32_t voff = col < nlim ? (uint32_t)(((wm * TI * 32 + odd) * ldc + col) * 2) : OOB;
+  for (int r4 = 0; r4 < 4; ++r4)
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+    for (int qp = 0; qp < 4; qp += 2) {
+      const auto s0 = __builtin_amdgcn_permlane32_swap(__float_as_uint(x0[4 * r4 + qp]),
+                                                       __float_as_uint(x1[4 * r4 + qp]), false, false);
+      const auto s1 = __builtin_amdgcn_permlane32_swap(__float_as_uint(x0[4 * r4 + qp + 1]),
+                                                       __float_as_uint(x1[4 * r4 + qp + 1]), false, false);
+      // s?[0]: row 32 i + 8 r4 + q (the lower half-wave's row), 64 columns;
+      // s?[1]: row 32 i + 8 r4 + 4 + q (the upper half-wave's row)
+      const int row = 32 * i + 8 * r4 + qp;
+      store_bf16_rows(__uint_as_float(s0[0]), __uint_as_float(s1[0]), r, voff, (uint32_t)(row * ldc * 2), sel);
+      store_bf16_rows(__uint_as_float(s0[1]), __uint_as_float(s1[1]), r, voff, (uint32_t)((row + 4) * ldc * 2),
+                      sel);
+    }
+}
+
+__device__ __forceinline__ void store_tile_bf16_lines(const Acc& acc, __amdgpu_buffer_rsrc_t r, int ldc, int nlim) {
+  static_assert(TJ % 2 == 0, "tiles are paired along N");
+  const int wn = (threadIdx.x >> 6) & 1;
 #pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4)
+  for (int jp = 0; jp < TJ; jp += 2)
 #pragma unroll
-        for (int qp = 0; qp < 4; qp += 2) {
-          const auto s0 = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc.t[i][jp][4 * r4 + qp]),
-                                                           __float_as_uint(acc.t[i][jp + 1][4 * r4 + qp]), false, false);
-          const auto s1 = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc.t[i][jp][4 * r4 + qp + 1]),
-                                                           __float_as_uint(acc.t[i][jp + 1][4 * r4 + qp + 1]), false,
-                                                           false);
-          // s?[0]: row 32 i + 8 r4 + q (the lower half-wave's row), 64 columns;
-          // s?[1]: row 32 i + 8 r4 + 4 + q (the upper half-wave's row)
-          const int row = 32 * i + 8 * r4 + qp;
-          store_bf16_rows(__uint_as_float(s0[0]), __uint_as_float(s1[0]), r, voff, (uint32_t)(row * ldc * 2), sel);
-          store_bf16_rows(__uint_as_float(s0[1]), __uint_as_float(s1[1]), r, voff, (uint32_t)((row + 4) * ldc * 2),
-                          sel);
-        }
-  }
+    for (int i = 0; i < TI; ++i) store_lines(acc.t[i][jp], acc.t[i][jp + 1], i, wn * TJ * 32 + 32 * jp, r, ldc, nlim);
 }
 
 // Store the wave's part of the tile.
@@ -1018,6 +1087,168 @@ __device__ __forceinline__ void store_unit(Acc& acc, const Sched& sc, int j, voi
     }
   if (threadIdx.x == 0) __hip_atomic_store(cnt, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+
+#if !MX_T256_SWAP
+// ------------------------------------------------------------ gated epilogue
+// With a gated row order the wave's MFMA tiles (i, 0), (i, 1) hold the gates
+// and (i, 2), (i, 3) the ups of its 64 hidden columns: register r of lane l
+// has both projections of one output.  The accumulators are only read (see
+// store_unit), 32x32 outputs at a time, and the activation is chosen once for
+// their 16 registers.  bf16 outputs leave in whole 128-byte lines: h, and dg
+// and du of the halves order, as in store_tile_bf16_lines; interleaved, a
+// lane's dg and du are neighbours, so one 4-byte store per lane writes the 32
+// pairs of two rows.
+__device__ __forceinline__ v16f gate16(const GateP& p, const v16f& g, const v16f& u) {
+  v16f h;
+  if (p.act == 0) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) h[e] = gate_forward<0>(p, g[e], u[e]);
+  } else if (p.act == 1) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) h[e] = gate_forward<1>(p, g[e], u[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) h[e] = gate_forward<2>(p, g[e], u[e]);
+  }
+  return h;
+}
+
+// g and u become dg and du.
+template <int ACT>
+__device__ __forceinline__ void gate16_backward_act(const GateP& p, v16f& g, v16f& u, const v16f& dh) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float dg, du;
+    gate_backward<ACT>(p, g[e], u[e], dh[e], dg, du);
+    g[e] = dg;
+    u[e] = du;
+  }
+}
+
+// Bounds-checked buffer over rows [row0, row0 + rows) of a row-major matrix,
+// columns [c0, c0 + cols).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t block_rsrc(const void* base, int64_t row0, int c0, int ld, int rows,
+                                                             int cols, int es) {
+  return rsrc(static_cast<const uint8_t*>(base) + (row0 * ld + c0) * es, (uint32_t)(((rows - 1) * ld + cols) * es));
+}
+
+// One MFMA tile (accumulator layout, row tile i), this lane's column `col`.
+__device__ __forceinline__ void store_block(const v16f& x, int i, int col, bool live, int ld, int bf16,
+                                            __amdgpu_buffer_rsrc_t r) {
+  const int lane = threadIdx.x & 63, wm = threadIdx.x >> 7, kh = lane >> 5;
+  const uint32_t at = (uint32_t)((wm * TI * 32 + 4 * kh) * ld + col);
+  if (bf16) {
+    const uint32_t vo = live ? 2 * at : OOB;
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (__bf16)x[e]), r, vo,
+                                            2 * (32 * i + 8 * (e >> 2) + (e & 3)) * ld, 0);
+  } else {
+    const uint32_t vo = live ? 4 * at : OOB;
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[e]), r, vo, 4 * (32 * i + 8 * (e >> 2) + (e & 3)) * ld,
+                                            0);
+  }
+}
+
+// One MFMA tile of a bf16 or float32 matrix in the accumulator layout.
+__device__ __forceinline__ v16f load_block(int i, int col, bool live, int ld, int bf16, __amdgpu_buffer_rsrc_t r) {
+  const int lane = threadIdx.x & 63, wm = threadIdx.x >> 7, kh = lane >> 5;
+  const uint32_t at = (uint32_t)((wm * TI * 32 + 4 * kh) * ld + col);
+  v16f x;
+  if (bf16) {
+    const uint32_t vo = live ? 2 * at : OOB;
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      x[e] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(
+                                 r, vo, 2 * (32 * i + 8 * (e >> 2) + (e & 3)) * ld, 0)
+                             << 16);
+  } else {
+    const uint32_t vo = live ? 4 * at : OOB;
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      x[e] = __uint_as_float(
+          __builtin_amdgcn_raw_buffer_load_b32(r, vo, 4 * (32 * i + 8 * (e >> 2) + (e & 3)) * ld, 0));
+  }
+  return x;
+}
+
+// Two MFMA tiles side by side (row tile i, the wave's 64 columns): whole lines
+// where the layout allows them.
+__device__ __forceinline__ void store_halves(const v16f& x0, const v16f& x1, int i, int ld, int cols, int bf16,
+                                             bool lines, __amdgpu_buffer_rsrc_t r) {
+  const int wn = (threadIdx.x >> 6) & 1, l32 = threadIdx.x & 31;
+  if (bf16 && lines) {
+    store_lines(x0, x1, i, wn * 64, r, ld, cols);
+    return;
+  }
+  const int col = wn * 64 + l32;
+  store_block(x0, i, col, col < cols, ld, bf16, r);
+  store_block(x1, i, col + 32, col + 32 < cols, ld, bf16, r);
+}
+
+template <bool BWD, int BMAP>
+__device__ __forceinline__ void store_tile_gate(const Acc& acc, const t256c::GateOut& q, int64_t row0, int n0,
+                                                int mlim, int nlim) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave >> 1, wn = wave & 1, l32 = lane & 31, kh = lane >> 5;
+  const int rows = mlim < 256 ? mlim : 256, cols = nlim < 128 ? nlim : 128;
+  const int eo = q.out_bf16 ? 2 : 4;
+  const bool even = (q.ldo & 1) == 0 && ((uintptr_t)q.out & 3) == 0;
+  if constexpr (!BWD) {
+    const __amdgpu_buffer_rsrc_t r = block_rsrc(q.out, row0, n0, q.ldo, rows, cols, eo);
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const v16f h0 = gate16(q.p, acc.t[i][0], acc.t[i][2]);
+      const v16f h1 = gate16(q.p, acc.t[i][1], acc.t[i][3]);
+      store_halves(h0, h1, i, q.ldo, cols, q.out_bf16, even && (cols & 1) == 0, r);
+    }
+  } else {
+    const int N = n0 + nlim, eh = q.dh_bf16 ? 2 : 4;
+    const __amdgpu_buffer_rsrc_t rh = block_rsrc(q.dH, row0, n0, q.lddh, rows, cols, eh);
+    // dg's columns and, interleaved, du's between them; as halves, du's are N further
+    const __amdgpu_buffer_rsrc_t rg = BMAP == t256c::B_HALVES
+                                          ? block_rsrc(q.out, row0, n0, q.ldo, rows, cols, eo)
+                                          : block_rsrc(q.out, row0, 2 * n0, q.ldo, rows, 2 * cols, eo);
+    const __amdgpu_buffer_rsrc_t ru = block_rsrc(q.out, row0, N + n0, q.ldo, rows, cols, eo);
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      v16f g[2], u[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int col = wn * 64 + 32 * j + l32;
+        const bool live = col < cols;
+        const v16f dh = load_block(i, col, live, q.lddh, q.dh_bf16, rh);
+        g[j] = acc.t[i][j];
+        u[j] = acc.t[i][j + 2];
+        if (q.p.act == 0) gate16_backward_act<0>(q.p, g[j], u[j], dh);
+        else if (q.p.act == 1) gate16_backward_act<1>(q.p, g[j], u[j], dh);
+        else gate16_backward_act<2>(q.p, g[j], u[j], dh);
+        if constexpr (BMAP == t256c::B_INTERLEAVED) {
+          if (q.out_bf16 && even) {
+            const uint32_t vo = live ? (uint32_t)(2 * ((wm * TI * 32 + 4 * kh) * q.ldo + 2 * col)) : OOB;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              __builtin_amdgcn_raw_buffer_store_b32(
+                  (uint32_t)__builtin_bit_cast(unsigned short, (__bf16)g[j][e]) |
+                      ((uint32_t)__builtin_bit_cast(unsigned short, (__bf16)u[j][e]) << 16),
+                  rg, vo, 2 * (32 * i + 8 * (e >> 2) + (e & 3)) * q.ldo, 0);
+          } else {
+            store_block(g[j], i, 2 * col, live, q.ldo, q.out_bf16, rg);
+            store_block(u[j], i, 2 * col + 1, live, q.ldo, q.out_bf16, rg);
+          }
+        }
+      }
+      if constexpr (BMAP == t256c::B_HALVES) {
+        const bool lines = even && (cols & 1) == 0 && (N & 1) == 0;
+        store_halves(g[0], g[1], i, q.ldo, cols, q.out_bf16, lines, rg);
+        store_halves(u[0], u[1], i, q.ldo, cols, q.out_bf16, lines, ru);
+      }
+    }
+  }
+}
+#endif
 
 #if MX_T256_SWAP
 // ------------------------------------------------------------ quantizing epilogue

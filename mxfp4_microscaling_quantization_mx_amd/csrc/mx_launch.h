@@ -120,6 +120,9 @@ struct TransposeArgs {
   int bits = 4;               // bits per element code (4, 6 or 8)
 };
 
+// Compute units of the current device (cached per device).
+int cu_count();
+
 hipError_t launch_quantize(const QuantArgs& a, hipStream_t st);
 
 // Clipping statistic: the elements that saturate when src is quantized with
@@ -233,5 +236,9 @@ size_t norm_backward_workspace(int64_t R, int64_t C);
 hipError_t launch_layer_norm_backward(const NormBwdArgs& a, hipStream_t st);
 hipError_t launch_dropout(const DropoutArgs& a, hipStream_t st);
 hipError_t launch_gated(const GatedArgs& a, hipStream_t st);
+// The gated block on the 256x256 MXFP4 pipeline (gated256.hip): whether it
+// takes this problem's types and layout, and its launch.
+bool gated256_layout_ok(const GatedArgs& a);
+hipError_t launch_gated256(const GatedArgs& a, hipStream_t st);
 
 }  // namespace mx
