@@ -8,14 +8,24 @@
 // Statistics and formulas are float32; the variance is taken from the centred
 // values (a difference of sums would cancel where |mean| >> the spread).
 //
-// A workgroup takes one row and reads it once per sum (the later reads come
-// from cache), so any width works.  The weight's gradient sums over rows:
-// each workgroup of a grid over (columns, row groups) adds every G-th row of
-// its columns in registers and stores one partial row [2][C] of dw and db; a
-// second launch adds the G partials in order.  No atomics: the same bits on
-// every run.
+// Both directions are bound by HBM bandwidth (bf16: 4 bytes per element
+// forward, 6 backward), so a row is read once and held in registers:
+//  * k_norm: 1, 4 or 16 waves per row, each lane VEC consecutive elements (16
+//    bytes where the rows allow it, else single elements) of every NV-th
+//    piece of the row.
+//  * k_norm_backward: 1 to 8 waves per row, workgroups of 8 waves walking the
+//    rows; each lane also keeps the sums of dw and db of its columns in
+//    registers over all its rows, adds them over the workgroup's row groups
+//    through LDS at the end and stores one partial row [2][C] per workgroup.
+//  * k_norm_any, k_norm_dx_any, k_norm_dw_any: rows too long for registers,
+//    read once per sum (the later reads come from cache), the weight's
+//    gradient by columns.
+// k_norm_dw_sum then adds the partial rows in order.  No atomics: the same
+// bits on every run.
 #include "mx_device.h"
 #include "mx_launch.h"
+
+#include <initializer_list>
 
 namespace mx {
 
@@ -145,6 +155,254 @@ __global__ __launch_bounds__(256) void k_norm_dw_any(NormBwdArgs a, int G) {
   p[a.C + c] = db;
 }
 
+// ------------------------------------------------------------ rows in registers
+// VEC consecutive elements at element i of a row (16 bytes, or one element).
+// The row pointer is wave-uniform and i 32 bits, so one scalar base and one
+// lane offset address the whole row.
+template <bool BF16, int VEC>
+struct Vec;
+template <>
+struct Vec<true, 8> {
+  uint4 w;
+  __device__ void load(const void* p, uint32_t i) {
+    w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+  }
+  __device__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  __device__ float get(int k) const {
+    const uint32_t v = (&w.x)[k >> 1];
+    return (k & 1) ? bf16hi(v) : bf16lo(v);
+  }
+  static __device__ void store(void* p, uint32_t i, const float* f) {
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      o[k] = (uint32_t)__builtin_bit_cast(unsigned short, (__bf16)f[2 * k]) |
+             ((uint32_t)__builtin_bit_cast(unsigned short, (__bf16)f[2 * k + 1]) << 16);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+};
+template <>
+struct Vec<false, 4> {
+  float4 w;
+  __device__ void load(const void* p, uint32_t i) { w = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i); }
+  __device__ void zero() { w = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ float get(int k) const { return (&w.x)[k]; }
+  static __device__ void store(void* p, uint32_t i, const float* f) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(f[0], f[1], f[2], f[3]);
+  }
+};
+template <bool BF16>
+struct Vec<BF16, 1> {
+  float w;
+  __device__ void load(const void* p, uint32_t i) {
+    w = BF16 ? bf16lo(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
+  }
+  __device__ void zero() { w = 0.0f; }
+  __device__ float get(int) const { return w; }
+  static __device__ void store(void* p, uint32_t i, const float* f) { st1<BF16>(p, i, f[0]); }
+};
+
+// VEC weight (or bias) entries at column c, or `none` without one.
+template <int VEC>
+__device__ __forceinline__ void load_param(const void* p, bool bf16, uint32_t c, float none, float f[VEC]) {
+  if (!p) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) f[k] = none;
+  } else if constexpr (VEC == 1) {
+    f[0] = ldw(p, bf16, c);
+  } else if (bf16) {
+    uint32_t w[VEC / 2];
+    if constexpr (VEC == 8) {
+      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + c);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + c);
+      w[0] = v.x, w[1] = v.y;
+    }
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) f[k] = (k & 1) ? bf16hi(w[k >> 1]) : bf16lo(w[k >> 1]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < VEC / 4; ++q) {
+      const float4 v = reinterpret_cast<const float4*>(static_cast<const float*>(p) + c)[q];
+      f[4 * q] = v.x, f[4 * q + 1] = v.y, f[4 * q + 2] = v.z, f[4 * q + 3] = v.w;
+    }
+  }
+}
+
+template <int WPR>
+constexpr int norm_threads() { return WPR > 4 ? 64 * WPR : 256; }
+
+template <bool BF16, int VEC, int NV, int WPR>
+__global__ __launch_bounds__(norm_threads<WPR>()) void k_norm(NormArgs a) {
+  constexpr int TH = norm_threads<WPR>(), RPB = TH / (64 * WPR);
+  static_assert(WPR == 1 || RPB == 1, "a row's waves are the workgroup, or one wave");
+  __shared__ float red[TH / 64];
+  const int sub = WPR == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  const uint32_t t = WPR == 1 ? threadIdx.x & 63 : threadIdx.x, C = (uint32_t)a.C;
+  constexpr int ES = BF16 ? 2 : 4;
+  for (int64_t r = (int64_t)blockIdx.x * RPB + sub; r < a.R; r += (int64_t)gridDim.x * RPB) {
+    const char* const xr = static_cast<const char*>(a.x) + r * a.ldx * ES;
+    char* const yr = static_cast<char*>(a.y) + r * a.ldy * ES;
+    float x[NV * VEC];
+    float s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const uint32_t c = (v * 64 * WPR + t) * VEC;
+      Vec<BF16, VEC> w;
+      if (c < C) w.load(xr, c);
+      else w.zero();
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) x[v * VEC + k] = w.get(k);
+    }
+#pragma unroll
+    for (int k = 0; k < NV * VEC; ++k) s = s + x[k];
+    const float mean = block_sum<WPR>(s, red) / (float)a.C;
+    float q = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const bool live = (v * 64 * WPR + t) * VEC < C;
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        x[v * VEC + k] = live ? x[v * VEC + k] - mean : 0.0f;
+        q = __builtin_fmaf(x[v * VEC + k], x[v * VEC + k], q);
+      }
+    }
+    const float rstd = 1.0f / __builtin_sqrtf(block_sum<WPR>(q, red) / (float)a.C + a.eps);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const uint32_t c = (v * 64 * WPR + t) * VEC;
+      if (c < C) {
+        float w[VEC], b[VEC], y[VEC];
+        load_param<VEC>(a.weight, a.w_bf16, c, 1.0f, w);
+        load_param<VEC>(a.bias, a.w_bf16, c, 0.0f, b);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) y[k] = __builtin_fmaf(x[v * VEC + k] * rstd, w[k], b[k]);
+        Vec<BF16, VEC>::store(yr, c, y);
+      }
+    }
+    if (t == 0) {
+      if (a.mean) a.mean[r] = mean;
+      if (a.rstd) a.rstd[r] = rstd;
+    }
+  }
+}
+
+constexpr int BW = 8;                           // waves of a backward workgroup
+
+// Two sums over a row group of WPR waves; red[2] alternates between the rows
+// of a workgroup's walk, so one barrier per row is enough (a wave can write
+// buffer i again only after the barrier of the row between, which every
+// reader of buffer i has passed on its way to).
+template <int WPR>
+__device__ __forceinline__ void group_sum2(float& p, float& q, float2 (*red)[BW], int turn) {
+  p = wave_sum(p);
+  q = wave_sum(q);
+  if (WPR == 1) return;
+  const int w = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) red[turn][w] = make_float2(p, q);
+  __syncthreads();
+  const int w0 = w / WPR * WPR;
+  p = red[turn][w0].x;
+  q = red[turn][w0].y;
+#pragma unroll
+  for (int i = 1; i < WPR; ++i) {
+    p = p + red[turn][w0 + i].x;
+    q = q + red[turn][w0 + i].y;
+  }
+}
+
+template <bool BF16, int VEC, int NV, int WPR>
+__global__ __launch_bounds__(64 * BW) void k_norm_backward(NormBwdArgs a) {
+  constexpr int RPB = BW / WPR, RL = 64 * WPR;  // row groups, lanes per row
+  __shared__ float2 red[2][BW];
+  __shared__ float part[2][RPB][RL * VEC];
+  const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / RL);
+  const uint32_t t = threadIdx.x % RL, C = (uint32_t)a.C;
+  constexpr int ES = BF16 ? 2 : 4;
+  const float inv = 1.0f / (float)a.C;
+  float dw[NV * VEC], db[NV * VEC];
+#pragma unroll
+  for (int k = 0; k < NV * VEC; ++k) dw[k] = db[k] = 0.0f;
+  int turn = 0;
+  // every wave of the workgroup makes the same number of passes (they share
+  // the barriers); a row group past the last row adds nothing
+  for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.R; base += (int64_t)gridDim.x * RPB, turn ^= 1) {
+    const int64_t r = base + sub;
+    const bool row = r < a.R;
+    const float mean = row ? a.mean[r] : 0.0f, rstd = row ? a.rstd[r] : 0.0f;
+    const char* const xr = static_cast<const char*>(a.x) + r * a.ldx * ES;
+    const char* const gr = static_cast<const char*>(a.dy) + r * a.lddy * ES;
+    char* const dr = static_cast<char*>(a.dx) + r * a.lddx * ES;
+    Vec<BF16, VEC> x[NV], g[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const uint32_t c = (v * RL + t) * VEC;
+      if (row && c < C) {
+        x[v].load(xr, c);
+        g[v].load(gr, c);
+      } else {
+        x[v].zero();
+        g[v].zero();
+      }
+    }
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const uint32_t c = (v * RL + t) * VEC;
+      float w[VEC];
+      load_param<VEC>(c < C ? a.weight : nullptr, a.w_bf16, c, 1.0f, w);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        const float dy = g[v].get(k), xh = (x[v].get(k) - mean) * rstd, gy = dy * w[k];
+        s1 = s1 + gy;
+        s2 = __builtin_fmaf(gy, xh, s2);
+        // a row past the end has dy = 0 and xh = 0; a column past it is not stored
+        dw[v * VEC + k] = __builtin_fmaf(dy, xh, dw[v * VEC + k]);
+        db[v * VEC + k] = db[v * VEC + k] + dy;
+      }
+    }
+    group_sum2<WPR>(s1, s2, red, turn);
+    if (a.dx && row) {
+      s1 = s1 * inv;
+      s2 = s2 * inv;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const uint32_t c = (v * RL + t) * VEC;
+        if (c < C) {
+          float w[VEC], o[VEC];
+          load_param<VEC>(a.weight, a.w_bf16, c, 1.0f, w);
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) {
+            const float xh = (x[v].get(k) - mean) * rstd;
+            o[k] = rstd * ((g[v].get(k) * w[k] - s1) - xh * s2);
+          }
+          Vec<BF16, VEC>::store(dr, c, o);
+        }
+      }
+    }
+  }
+  if (!a.workspace) return;
+  float* const out = a.workspace + (int64_t)blockIdx.x * 2 * a.C;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      part[0][sub][t * VEC + k] = dw[v * VEC + k];
+      part[1][sub][t * VEC + k] = db[v * VEC + k];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * RL * VEC; i += 64 * BW) {
+      const int which = i / (RL * VEC), j = i - which * RL * VEC, c = v * RL * VEC + j;
+      float s = part[which][0][j];
+#pragma unroll
+      for (int q = 1; q < RPB; ++q) s = s + part[which][q][j];
+      if (c < a.C) out[(int64_t)which * a.C + c] = s;
+    }
+    __syncthreads();
+  }
+}
+
 // dw and db from the G partial rows: 64 columns per workgroup, 16 waves each
 // adding every 16th partial, their sums added in wave order.
 __global__ __launch_bounds__(1024) void k_norm_dw_sum(const float* __restrict__ part, int G, int64_t C,
@@ -167,43 +425,131 @@ __global__ __launch_bounds__(1024) void k_norm_dw_sum(const float* __restrict__ 
   }
 }
 
-// Partial rows of dw and db: enough row groups to fill the chip, fewer where a
-// partial row is itself long.
-int64_t norm_groups(int64_t R, int64_t C) {
-  const int64_t most = C <= 24576 ? 512 : 64;
-  return R < most ? R : most;
+// Partial rows of dw and db: workgroups of k_norm_backward (one per CU: its
+// registers allow no more) and row groups of k_norm_dw_any.
+constexpr int64_t MOST_GROUPS = 256;
+int64_t norm_groups(int64_t R) { return R < MOST_GROUPS ? R : MOST_GROUPS; }
+
+// Whether rows of C elements at these strides and addresses can be read 16
+// bytes at a time, weights included.
+bool norm_vec(int64_t C, bool bf16, std::initializer_list<int64_t> ld, std::initializer_list<const void*> p) {
+  const int64_t vec = bf16 ? 8 : 4;
+  bool ok = C % vec == 0;
+  for (int64_t l : ld) ok = ok && l % vec == 0;
+  for (const void* q : p) ok = ok && (uintptr_t)q % 16 == 0;
+  return ok;
 }
+
+template <bool BF16, int VEC, int NV, int WPR>
+int64_t start_norm(const NormArgs& a, hipStream_t st) {
+  constexpr int RPB = norm_threads<WPR>() / (64 * WPR);
+  hipLaunchKernelGGL((k_norm<BF16, VEC, NV, WPR>), dim3(row_grid((a.R + RPB - 1) / RPB)), dim3(norm_threads<WPR>()), 0,
+                     st, a);
+  return 1;
+}
+
+template <bool BF16, int VEC, int NV, int WPR>
+int64_t start_norm_backward(const NormBwdArgs& a, hipStream_t st) {
+  constexpr int RPB = BW / WPR;
+  const int64_t G = norm_groups((a.R + RPB - 1) / RPB);
+  hipLaunchKernelGGL((k_norm_backward<BF16, VEC, NV, WPR>), dim3((unsigned)G), dim3(64 * BW), 0, st, a);
+  return G;
+}
+
+// Launch with the first of the compiled (pieces per lane, waves per row) that
+// holds a row of C elements; 0 if the row is longer than all of them, else the
+// launch's partial rows (backward).
+#define MX_NV(K_, NV_, WPR_) \
+  if (a.C <= (int64_t)(NV_) * VEC * 64 * (WPR_)) return K_<BF16, VEC, NV_, WPR_>(a, st);
+
+template <bool BF16, int VEC>
+int64_t try_norm(const NormArgs& a, hipStream_t st) {
+  if constexpr (VEC == 8) {
+    MX_NV(start_norm, 1, 1) MX_NV(start_norm, 2, 1) MX_NV(start_norm, 3, 1) MX_NV(start_norm, 4, 1)
+    MX_NV(start_norm, 5, 1) MX_NV(start_norm, 6, 1)
+    MX_NV(start_norm, 2, 4) MX_NV(start_norm, 3, 4) MX_NV(start_norm, 4, 4) MX_NV(start_norm, 6, 4)
+    MX_NV(start_norm, 2, 16) MX_NV(start_norm, 4, 16)
+  } else if constexpr (VEC == 4) {
+    MX_NV(start_norm, 1, 1) MX_NV(start_norm, 2, 1) MX_NV(start_norm, 4, 1) MX_NV(start_norm, 6, 1)
+    MX_NV(start_norm, 8, 1) MX_NV(start_norm, 12, 1)
+    MX_NV(start_norm, 4, 4) MX_NV(start_norm, 6, 4) MX_NV(start_norm, 8, 4) MX_NV(start_norm, 12, 4)
+    MX_NV(start_norm, 4, 16) MX_NV(start_norm, 6, 16)
+  } else {
+    MX_NV(start_norm, 2, 1) MX_NV(start_norm, 4, 1) MX_NV(start_norm, 8, 1) MX_NV(start_norm, 12, 1)
+    MX_NV(start_norm, 18, 1) MX_NV(start_norm, 24, 1) MX_NV(start_norm, 8, 4) MX_NV(start_norm, 12, 4)
+    MX_NV(start_norm, 16, 4) MX_NV(start_norm, 24, 4) MX_NV(start_norm, 8, 16)
+  }
+  return 0;
+}
+
+template <bool BF16, int VEC>
+int64_t try_norm_backward(const NormBwdArgs& a, hipStream_t st) {
+  if constexpr (VEC == 8) {
+    MX_NV(start_norm_backward, 1, 1) MX_NV(start_norm_backward, 2, 1) MX_NV(start_norm_backward, 3, 1)
+    MX_NV(start_norm_backward, 4, 1) MX_NV(start_norm_backward, 5, 1) MX_NV(start_norm_backward, 6, 1)
+    MX_NV(start_norm_backward, 4, 2) MX_NV(start_norm_backward, 5, 2) MX_NV(start_norm_backward, 6, 2)
+    MX_NV(start_norm_backward, 4, 4) MX_NV(start_norm_backward, 6, 4) MX_NV(start_norm_backward, 4, 8)
+    MX_NV(start_norm_backward, 6, 8)
+  } else if constexpr (VEC == 4) {
+    MX_NV(start_norm_backward, 1, 1) MX_NV(start_norm_backward, 2, 1) MX_NV(start_norm_backward, 4, 1)
+    MX_NV(start_norm_backward, 6, 1) MX_NV(start_norm_backward, 8, 1)
+    MX_NV(start_norm_backward, 6, 2) MX_NV(start_norm_backward, 8, 2) MX_NV(start_norm_backward, 6, 4)
+    MX_NV(start_norm_backward, 8, 4) MX_NV(start_norm_backward, 6, 8) MX_NV(start_norm_backward, 8, 8)
+  } else {
+    MX_NV(start_norm_backward, 2, 1) MX_NV(start_norm_backward, 4, 1) MX_NV(start_norm_backward, 8, 1)
+    MX_NV(start_norm_backward, 12, 1) MX_NV(start_norm_backward, 18, 1) MX_NV(start_norm_backward, 24, 1)
+    MX_NV(start_norm_backward, 18, 2) MX_NV(start_norm_backward, 24, 2) MX_NV(start_norm_backward, 18, 4)
+    MX_NV(start_norm_backward, 24, 4) MX_NV(start_norm_backward, 18, 8) MX_NV(start_norm_backward, 24, 8)
+  }
+  return 0;
+}
+#undef MX_NV
 
 }  // namespace
 
 size_t norm_backward_workspace(int64_t R, int64_t C) {
-  return (size_t)norm_groups(R, C) * 2 * (size_t)C * sizeof(float);
+  return (size_t)norm_groups(R) * 2 * (size_t)C * sizeof(float);
 }
 
 hipError_t launch_layer_norm(const NormArgs& a, hipStream_t st) {
   if (a.R == 0 || a.C == 0) return hipSuccess;
-  if (a.bf16) hipLaunchKernelGGL((k_norm_any<true>), dim3(row_grid(a.R)), dim3(64 * LW), 0, st, a);
-  else hipLaunchKernelGGL((k_norm_any<false>), dim3(row_grid(a.R)), dim3(64 * LW), 0, st, a);
+  const bool vec = norm_vec(a.C, a.bf16, {a.ldx, a.ldy}, {a.x, a.y, a.weight, a.bias});
+  const int64_t held = a.bf16 ? (vec ? try_norm<true, 8>(a, st) : try_norm<true, 1>(a, st))
+                           : (vec ? try_norm<false, 4>(a, st) : try_norm<false, 1>(a, st));
+  if (!held) {
+    if (a.bf16) hipLaunchKernelGGL((k_norm_any<true>), dim3(row_grid(a.R)), dim3(64 * LW), 0, st, a);
+    else hipLaunchKernelGGL((k_norm_any<false>), dim3(row_grid(a.R)), dim3(64 * LW), 0, st, a);
+  }
   return hipGetLastError();
 }
 
-hipError_t launch_layer_norm_backward(const NormBwdArgs& a, hipStream_t st) {
+hipError_t launch_layer_norm_backward(const NormBwdArgs& args, hipStream_t st) {
+  NormBwdArgs a = args;
   if (a.C == 0) return hipSuccess;
-  // the weight's gradients first: dx may be written over dy or x
-  if (a.dweight || a.dbias) {
-    const int G = (int)norm_groups(a.R, a.C);
-    if (G > 0) {
-      const dim3 grid((unsigned)((a.C + 255) / 256), (unsigned)G);
-      if (a.bf16) hipLaunchKernelGGL((k_norm_dw_any<true>), grid, dim3(256), 0, st, a, G);
-      else hipLaunchKernelGGL((k_norm_dw_any<false>), grid, dim3(256), 0, st, a, G);
+  const bool sums = a.dweight || a.dbias;
+  if (!sums) a.workspace = nullptr;
+  int64_t G = 0;
+  if (a.R > 0 && (sums || a.dx)) {
+    const bool vec = norm_vec(a.C, a.bf16, {a.ldx, a.lddy, a.dx ? a.lddx : 0}, {a.x, a.dy, a.dx, a.weight});
+    G = a.bf16 ? (vec ? try_norm_backward<true, 8>(a, st) : try_norm_backward<true, 1>(a, st))
+               : (vec ? try_norm_backward<false, 4>(a, st) : try_norm_backward<false, 1>(a, st));
+    if (G == 0) {
+      // the weight's gradients first: dx may be written over dy or x
+      if (sums) {
+        G = norm_groups(a.R);
+        const dim3 grid((unsigned)((a.C + 255) / 256), (unsigned)G);
+        if (a.bf16) hipLaunchKernelGGL((k_norm_dw_any<true>), grid, dim3(256), 0, st, a, (int)G);
+        else hipLaunchKernelGGL((k_norm_dw_any<false>), grid, dim3(256), 0, st, a, (int)G);
+      }
+      if (a.dx) {
+        if (a.bf16) hipLaunchKernelGGL((k_norm_dx_any<true>), dim3(row_grid(a.R)), dim3(64 * LW), 0, st, a);
+        else hipLaunchKernelGGL((k_norm_dx_any<false>), dim3(row_grid(a.R)), dim3(64 * LW), 0, st, a);
+      }
     }
-    hipLaunchKernelGGL(k_norm_dw_sum, dim3((unsigned)((a.C + 63) / 64), 2), dim3(1024), 0, st, a.workspace, G, a.C,
-                       a.dweight, a.dbias, (int)a.w_bf16);
   }
-  if (a.dx && a.R > 0) {
-    if (a.bf16) hipLaunchKernelGGL((k_norm_dx_any<true>), dim3(row_grid(a.R)), dim3(64 * LW), 0, st, a);
-    else hipLaunchKernelGGL((k_norm_dx_any<false>), dim3(row_grid(a.R)), dim3(64 * LW), 0, st, a);
-  }
+  if (sums)
+    hipLaunchKernelGGL(k_norm_dw_sum, dim3((unsigned)((a.C + 63) / 64), 2), dim3(1024), 0, st, a.workspace, (int)G,
+                       a.C, a.dweight, a.dbias, (int)a.w_bf16);
   return hipGetLastError();
 }
 
