@@ -28,7 +28,7 @@ CFLAGS = [
     "-ffp-contract=off", "-Wall", "-Wno-unused-function",
 ]
 SOURCES = ["mx_api.cpp", "quantize.hip", "dequantize.hip", "transpose.hip", "gemm.hip", "gemm_splitk.hip", "clip.hip",
-           "gated.hip", "gated256.hip", "norm.hip", "dropout.hip"]
+           "gated.hip", "gated256.hip", "gated_f8.hip", "norm.hip", "dropout.hip"]
 
 
 def _run(cmd):

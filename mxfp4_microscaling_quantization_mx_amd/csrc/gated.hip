@@ -206,6 +206,7 @@ hipError_t launch_direct_b(const GatedArgs& a, hipStream_t st) {
 hipError_t launch_gated(const GatedArgs& a, hipStream_t st) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
   if (a.M >= 256 && a.N >= 128 && gated256_layout_ok(a)) return launch_gated256(a, st);
+  if (a.M >= 256 && a.N >= 128 && gated_f8_layout_ok(a)) return launch_gated_f8(a, st);
   switch (a.a_elem) {
     case 1: return launch_direct_b<1>(a, st);
     case 2: return launch_direct_b<2>(a, st);

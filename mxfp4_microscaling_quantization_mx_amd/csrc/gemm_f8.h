@@ -234,12 +234,16 @@ __device__ __forceinline__ void f8_compute(v16f acc[2][4], uint32_t slot, uint32
 // first stage loads into the free slot while the current tile's last stage is
 // multiplied and its result stored.
 // OUT: 0 float32, 1 bf16, 2 the quantizing epilogue (MXFP4 codes and scale
-// bytes along N into qo, from the swapped-operand accumulators).
+// bytes along N into qo, from the swapped-operand accumulators), 3 the gated
+// block's epilogue (go: forward, or with dH backward; `halves` its row order).
 template <int FA, int FB, int OUT, class Sched>
 __device__ __forceinline__ void run_f8(const Sched& sc, const MxOperand& A, const MxOperand& B, int K, void* C,
                                        int64_t ldc, int a_2d, int b_2d, uint8_t* slots, uint32_t* sws,
-                                       const t256::QOut& qo = t256::QOut{}) {
+                                       const t256::QOut& qo = t256::QOut{}, const t256c::GateOut* go = nullptr,
+                                       int halves = 0) {
   constexpr bool OUT_BF16 = OUT == 1;
+  constexpr bool GATED = OUT == 3;
+  static_assert(GATED == (Sched::BMAP != t256c::B_ROWS), "the gated epilogue needs the gated row order");
   constexpr bool SWAP = OUT == 2;
   const int ntiles = sc.count();
   const int tid = threadIdx.x, lane = tid & 63;
@@ -264,22 +268,33 @@ __device__ __forceinline__ void run_f8(const Sched& sc, const MxOperand& A, cons
     mlim = ti.M - ti.m0;
     nlim = ti.N - ti.n0;
     const int arows = mlim < 256 ? mlim : 256, brows = nlim < 256 ? nlim : 256;
+    // row of B for LDS row r, from the tile's first row, or -1 past the end
+    // (gated: from the operand's first row, gates and ups in turn)
+    auto b_row = [&](int r) {
+      if constexpr (!GATED) return r < brows ? r : -1;
+      else return halves ? t256c::b_row<t256c::B_HALVES>(ti.n0, ti.N, r)
+                         : t256c::b_row<t256c::B_INTERLEAVED>(ti.n0, ti.N, r);
+    };
     L.ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(ti.a_codes) + (int64_t)ti.m0 * A.ld_codes, 0,
                                              (uint32_t)(arows * A.ld_codes), 0x00020000);
-    L.rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(ti.b_codes) + (int64_t)ti.n0 * B.ld_codes, 0,
-                                             (uint32_t)(brows * B.ld_codes), 0x00020000);
+    L.rb = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(ti.b_codes) + (GATED ? 0 : (int64_t)ti.n0 * B.ld_codes), 0,
+        (uint32_t)((GATED ? 2 * ti.N : brows) * B.ld_codes), 0x00020000);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int row = 8 * (4 * wave + t) + (lane >> 3);
       L.c[t] = crow[t];
       L.va[t] = row < arows ? (uint32_t)(row * A.ld_codes + 16 * crow[t]) : MX_OOB;
-      L.vb[t] = row < brows ? (uint32_t)(row * B.ld_codes + 16 * crow[t]) : MX_OOB;
+      const int rb = b_row(row);
+      L.vb[t] = rb >= 0 ? (uint32_t)(rb * B.ld_codes + 16 * crow[t]) : MX_OOB;
     }
-    const int r0 = sA ? ti.m0 : ti.n0, rows = sA ? arows : brows;
+    const int r0 = sA ? ti.m0 : GATED ? 0 : ti.n0;
+    const int sr = sA ? (srow < arows ? srow : -1) : b_row(srow);
+    const int srows = sA || !GATED ? 256 : 2 * ti.N;
     const uint8_t* sbase = (sA ? ti.a_scales : ti.b_scales) + (int64_t)(s2d ? (r0 >> 5) : r0) * lds_s;
-    L.rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(sbase), 0, (uint32_t)((s2d ? 8 : 256) * lds_s),
+    L.rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(sbase), 0, (uint32_t)((s2d ? srows / 32 : srows) * lds_s),
                                              0x00020000);
-    L.so = srow < rows ? (uint32_t)((s2d ? (srow >> 5) : srow) * lds_s) : MX_OOB;
+    L.so = sr >= 0 ? (uint32_t)((s2d ? (sr >> 5) : sr) * lds_s) : MX_OOB;
     crow0 = ti.c_row0;
     n0 = ti.n0;
   };
@@ -323,6 +338,14 @@ __device__ __forceinline__ void run_f8(const Sched& sc, const MxOperand& A, cons
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) q.t[i][jj] = acc.t[i][jj];
       t256s::store_tile_mx(q, qo, (int)c0, n0, mlim, nlim);
+    } else if constexpr (GATED) {
+      const t256c::GateOut q = t256c::load_gate_out(go);
+      if (q.dH) {
+        if (halves) t256::store_tile_gate<true, t256c::B_HALVES>(acc, q, c0, n0, mlim, nlim);
+        else t256::store_tile_gate<true, t256c::B_INTERLEAVED>(acc, q, c0, n0, mlim, nlim);
+      } else {
+        t256::store_tile_gate<false, t256c::B_INTERLEAVED>(acc, q, c0, n0, mlim, nlim);
+      }
     } else {
       constexpr int ES = OUT_BF16 ? 2 : 4;
       t256::store_tile<OUT_BF16>(acc, static_cast<uint8_t*>(C) + (c0 * ldc + n0) * ES, (int)ldc, mlim, nlim);

@@ -1093,36 +1093,36 @@ __device__ __forceinline__ void store_unit(Acc& acc, const Sched& sc, int j, voi
 // With a gated row order the wave's MFMA tiles (i, 0), (i, 1) hold the gates
 // and (i, 2), (i, 3) the ups of its 64 hidden columns: register r of lane l
 // has both projections of one output.  The accumulators are only read (see
-// store_unit), 32x32 outputs at a time, and the activation is chosen once for
-// their 16 registers.  bf16 outputs leave in whole 128-byte lines: h, and dg
-// and du of the halves order, as in store_tile_bf16_lines; interleaved, a
-// lane's dg and du are neighbours, so one 4-byte store per lane writes the 32
-// pairs of two rows.
-__device__ __forceinline__ v16f gate16(const GateP& p, const v16f& g, const v16f& u) {
-  v16f h;
-  if (p.act == 0) {
+// store_unit), four rows of both column tiles at a time, which keeps what the
+// epilogue adds to the pipeline's registers small; the activation is chosen
+// once per such piece.
+//
+// bf16 matrices go in and out in whole 128-byte lines where their layout
+// allows it: h, dH, and dg and du of the halves order through the exchanges
+// of store_bf16_rows (which undo themselves); interleaved, a lane's dg and du
+// are neighbours, so one 4-byte store per lane writes the 32 pairs of two
+// rows.  The 32 words of dH are all requested before the first is used.
+struct GateTile {
+  float t[2][4];                           // column tile, row 4 kh + q
+};
+
+template <int ACT>
+__device__ __forceinline__ void gate_piece_act(const GateP& p, const Acc& acc, int i, int r4, GateTile& h) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) h[e] = gate_forward<0>(p, g[e], u[e]);
-  } else if (p.act == 1) {
+  for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) h[e] = gate_forward<1>(p, g[e], u[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) h[e] = gate_forward<2>(p, g[e], u[e]);
-  }
-  return h;
+    for (int q = 0; q < 4; ++q)
+      h.t[j][q] = gate_forward<ACT>(p, acc.t[i][j][4 * r4 + q], acc.t[i][j + 2][4 * r4 + q]);
 }
 
-// g and u become dg and du.
 template <int ACT>
-__device__ __forceinline__ void gate16_backward_act(const GateP& p, v16f& g, v16f& u, const v16f& dh) {
+__device__ __forceinline__ void gate_piece_backward_act(const GateP& p, const Acc& acc, int i, int r4,
+                                                        const GateTile& dh, GateTile& dg, GateTile& du) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    float dg, du;
-    gate_backward<ACT>(p, g[e], u[e], dh[e], dg, du);
-    g[e] = dg;
-    u[e] = du;
-  }
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      gate_backward<ACT>(p, acc.t[i][j][4 * r4 + q], acc.t[i][j + 2][4 * r4 + q], dh.t[j][q], dg.t[j][q], du.t[j][q]);
 }
 
 // Bounds-checked buffer over rows [row0, row0 + rows) of a row-major matrix,
@@ -1132,120 +1132,184 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t block_rsrc(const void* base, i
   return rsrc(static_cast<const uint8_t*>(base) + (row0 * ld + c0) * es, (uint32_t)(((rows - 1) * ld + cols) * es));
 }
 
-// One MFMA tile (accumulator layout, row tile i), this lane's column `col`.
-__device__ __forceinline__ void store_block(const v16f& x, int i, int col, bool live, int ld, int bf16,
-                                            __amdgpu_buffer_rsrc_t r) {
-  const int lane = threadIdx.x & 63, wm = threadIdx.x >> 7, kh = lane >> 5;
-  const uint32_t at = (uint32_t)((wm * TI * 32 + 4 * kh) * ld + col);
-  if (bf16) {
-    const uint32_t vo = live ? 2 * at : OOB;
+// This lane's place in the 256-row tile: its column in the accumulator layout
+// (32-column tiles) and in the line layout (pairs of columns), its first rows.
+struct GatePlace {
+  int col, line_col, row, line_row;
+  uint32_t sel;
+};
+
+__device__ __forceinline__ GatePlace gate_place() {
+  // opaque to the compiler, which would otherwise work these out before the
+  // pipeline and hold them in registers that it does not have
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid & 63, wave = tid >> 6, odd = lane & 1;
+  const int wm = wave >> 1, wn = wave & 1;
+  return {wn * 64 + (lane & 31), wn * 64 + (lane & ~1), wm * TI * 32 + 4 * (lane >> 5), wm * TI * 32 + odd,
+          odd ? 0x03020706u : 0x05040100u};
+}
+
+// Columns col + 32 j (times step, plus at) of the piece's four rows, one
+// element at a time.
+__device__ __forceinline__ void store_piece(const GateTile& x, int i, int r4, const GatePlace& pl, int step, int at,
+                                            int cols, int ld, int bf16, __amdgpu_buffer_rsrc_t r) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (__bf16)x[e]), r, vo,
-                                            2 * (32 * i + 8 * (e >> 2) + (e & 3)) * ld, 0);
-  } else {
-    const uint32_t vo = live ? 4 * at : OOB;
+  for (int j = 0; j < 2; ++j) {
+    const bool live = pl.col + 32 * j < cols;
+    const uint32_t e = (uint32_t)(pl.row * ld + (pl.col + 32 * j) * step + at);
+    if (bf16) {
+      const uint32_t vo = live ? 2 * e : OOB;
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[e]), r, vo, 4 * (32 * i + 8 * (e >> 2) + (e & 3)) * ld,
-                                            0);
+      for (int q = 0; q < 4; ++q)
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (__bf16)x.t[j][q]), r, vo,
+                                              2 * (32 * i + 8 * r4 + q) * ld, 0);
+    } else {
+      const uint32_t vo = live ? 4 * e : OOB;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x.t[j][q]), r, vo, 4 * (32 * i + 8 * r4 + q) * ld, 0);
+    }
   }
 }
 
-// One MFMA tile of a bf16 or float32 matrix in the accumulator layout.
-__device__ __forceinline__ v16f load_block(int i, int col, bool live, int ld, int bf16, __amdgpu_buffer_rsrc_t r) {
-  const int lane = threadIdx.x & 63, wm = threadIdx.x >> 7, kh = lane >> 5;
-  const uint32_t at = (uint32_t)((wm * TI * 32 + 4 * kh) * ld + col);
-  v16f x;
-  if (bf16) {
-    const uint32_t vo = live ? 2 * at : OOB;
+__device__ __forceinline__ void load_piece(GateTile& x, int i, int r4, const GatePlace& pl, int cols, int ld, int bf16,
+                                           __amdgpu_buffer_rsrc_t r) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      x[e] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(
-                                 r, vo, 2 * (32 * i + 8 * (e >> 2) + (e & 3)) * ld, 0)
-                             << 16);
-  } else {
-    const uint32_t vo = live ? 4 * at : OOB;
+  for (int j = 0; j < 2; ++j) {
+    const bool live = pl.col + 32 * j < cols;
+    const uint32_t e = (uint32_t)(pl.row * ld + pl.col + 32 * j);
+    if (bf16) {
+      const uint32_t vo = live ? 2 * e : OOB;
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      x[e] = __uint_as_float(
-          __builtin_amdgcn_raw_buffer_load_b32(r, vo, 4 * (32 * i + 8 * (e >> 2) + (e & 3)) * ld, 0));
+      for (int q = 0; q < 4; ++q)
+        x.t[j][q] = __uint_as_float(
+            (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, vo, 2 * (32 * i + 8 * r4 + q) * ld, 0) << 16);
+    } else {
+      const uint32_t vo = live ? 4 * e : OOB;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        x.t[j][q] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, vo, 4 * (32 * i + 8 * r4 + q) * ld, 0));
+    }
   }
-  return x;
 }
 
-// Two MFMA tiles side by side (row tile i, the wave's 64 columns): whole lines
-// where the layout allows them.
-__device__ __forceinline__ void store_halves(const v16f& x0, const v16f& x1, int i, int ld, int cols, int bf16,
-                                             bool lines, __amdgpu_buffer_rsrc_t r) {
-  const int wn = (threadIdx.x >> 6) & 1, l32 = threadIdx.x & 31;
-  if (bf16 && lines) {
-    store_lines(x0, x1, i, wn * 64, r, ld, cols);
-    return;
+// The piece's four rows x 2 (lower and upper half-wave) in whole lines.
+__device__ __forceinline__ void store_piece_lines(const GateTile& x, int i, int r4, const GatePlace& pl, uint32_t voff,
+                                                  int ld, __amdgpu_buffer_rsrc_t r) {
+#pragma unroll
+  for (int qp = 0; qp < 4; qp += 2) {
+    const auto s0 = __builtin_amdgcn_permlane32_swap(__float_as_uint(x.t[0][qp]), __float_as_uint(x.t[1][qp]), false,
+                                                     false);
+    const auto s1 = __builtin_amdgcn_permlane32_swap(__float_as_uint(x.t[0][qp + 1]), __float_as_uint(x.t[1][qp + 1]),
+                                                     false, false);
+    const int row = 32 * i + 8 * r4 + qp;
+    store_bf16_rows(__uint_as_float(s0[0]), __uint_as_float(s1[0]), r, voff, (uint32_t)(row * ld * 2), pl.sel);
+    store_bf16_rows(__uint_as_float(s0[1]), __uint_as_float(s1[1]), r, voff, (uint32_t)((row + 4) * ld * 2), pl.sel);
   }
-  const int col = wn * 64 + l32;
-  store_block(x0, i, col, col < cols, ld, bf16, r);
-  store_block(x1, i, col + 32, col + 32 < cols, ld, bf16, r);
+}
+
+// The reverse: four words loaded as lines back to the accumulator layout.
+__device__ __forceinline__ void unpack_piece(const uint32_t w[4], uint32_t sel, GateTile& x) {
+#pragma unroll
+  for (int qp = 0; qp < 4; qp += 2) {
+    uint32_t p[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t v = w[qp + h];        // rows row + 4 h (low half) and row + 4 h + 1 once exchanged
+      const uint32_t n = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false);
+      p[h] = __builtin_amdgcn_perm(n, v, sel);
+    }
+    const auto s0 = __builtin_amdgcn_permlane32_swap(p[0] << 16, p[1] << 16, false, false);
+    const auto s1 = __builtin_amdgcn_permlane32_swap(p[0] & 0xFFFF0000u, p[1] & 0xFFFF0000u, false, false);
+    x.t[0][qp] = __uint_as_float(s0[0]);
+    x.t[1][qp] = __uint_as_float(s0[1]);
+    x.t[0][qp + 1] = __uint_as_float(s1[0]);
+    x.t[1][qp + 1] = __uint_as_float(s1[1]);
+  }
 }
 
 template <bool BWD, int BMAP>
 __device__ __forceinline__ void store_tile_gate(const Acc& acc, const t256c::GateOut& q, int64_t row0, int n0,
                                                 int mlim, int nlim) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave >> 1, wn = wave & 1, l32 = lane & 31, kh = lane >> 5;
+  const GatePlace pl = gate_place();
   const int rows = mlim < 256 ? mlim : 256, cols = nlim < 128 ? nlim : 128;
   const int eo = q.out_bf16 ? 2 : 4;
-  const bool even = (q.ldo & 1) == 0 && ((uintptr_t)q.out & 3) == 0;
+  const bool even = q.out_bf16 && (q.ldo & 1) == 0 && ((uintptr_t)q.out & 3) == 0;
+  const bool line_in = pl.line_col < cols;
   if constexpr (!BWD) {
     const __amdgpu_buffer_rsrc_t r = block_rsrc(q.out, row0, n0, q.ldo, rows, cols, eo);
+    const bool lines = even && (cols & 1) == 0;
+    const uint32_t voff = line_in ? (uint32_t)((pl.line_row * q.ldo + pl.line_col) * 2) : OOB;
 #pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      const v16f h0 = gate16(q.p, acc.t[i][0], acc.t[i][2]);
-      const v16f h1 = gate16(q.p, acc.t[i][1], acc.t[i][3]);
-      store_halves(h0, h1, i, q.ldo, cols, q.out_bf16, even && (cols & 1) == 0, r);
-    }
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        GateTile h;
+        if (q.p.act == 0) gate_piece_act<0>(q.p, acc, i, r4, h);
+        else if (q.p.act == 1) gate_piece_act<1>(q.p, acc, i, r4, h);
+        else gate_piece_act<2>(q.p, acc, i, r4, h);
+        if (lines) store_piece_lines(h, i, r4, pl, voff, q.ldo, r);
+        else store_piece(h, i, r4, pl, 1, 0, cols, q.ldo, q.out_bf16, r);
+      }
   } else {
     const int N = n0 + nlim, eh = q.dh_bf16 ? 2 : 4;
     const __amdgpu_buffer_rsrc_t rh = block_rsrc(q.dH, row0, n0, q.lddh, rows, cols, eh);
+    const bool hlines = q.dh_bf16 && ((q.lddh | cols) & 1) == 0 && ((uintptr_t)q.dH & 3) == 0;
+    uint32_t w[TI][4][4];
+    if (hlines) {
+      const uint32_t vo = line_in ? (uint32_t)((pl.line_row * q.lddh + pl.line_col) * 2) : OOB;
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[i][r4][k] = __builtin_amdgcn_raw_buffer_load_b32(
+                rh, vo, 2 * (32 * i + 8 * r4 + (k & 2) + 4 * (k & 1)) * q.lddh, 0);
+    }
     // dg's columns and, interleaved, du's between them; as halves, du's are N further
     const __amdgpu_buffer_rsrc_t rg = BMAP == t256c::B_HALVES
                                           ? block_rsrc(q.out, row0, n0, q.ldo, rows, cols, eo)
                                           : block_rsrc(q.out, row0, 2 * n0, q.ldo, rows, 2 * cols, eo);
     const __amdgpu_buffer_rsrc_t ru = block_rsrc(q.out, row0, N + n0, q.ldo, rows, cols, eo);
+    const bool lines = even && (cols & 1) == 0 && (N & 1) == 0;
+    const uint32_t voff = line_in ? (uint32_t)((pl.line_row * q.ldo + pl.line_col) * 2) : OOB;
 #pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      v16f g[2], u[2];
+    for (int i = 0; i < TI; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int col = wn * 64 + 32 * j + l32;
-        const bool live = col < cols;
-        const v16f dh = load_block(i, col, live, q.lddh, q.dh_bf16, rh);
-        g[j] = acc.t[i][j];
-        u[j] = acc.t[i][j + 2];
-        if (q.p.act == 0) gate16_backward_act<0>(q.p, g[j], u[j], dh);
-        else if (q.p.act == 1) gate16_backward_act<1>(q.p, g[j], u[j], dh);
-        else gate16_backward_act<2>(q.p, g[j], u[j], dh);
-        if constexpr (BMAP == t256c::B_INTERLEAVED) {
-          if (q.out_bf16 && even) {
-            const uint32_t vo = live ? (uint32_t)(2 * ((wm * TI * 32 + 4 * kh) * q.ldo + 2 * col)) : OOB;
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              __builtin_amdgcn_raw_buffer_store_b32(
-                  (uint32_t)__builtin_bit_cast(unsigned short, (__bf16)g[j][e]) |
-                      ((uint32_t)__builtin_bit_cast(unsigned short, (__bf16)u[j][e]) << 16),
-                  rg, vo, 2 * (32 * i + 8 * (e >> 2) + (e & 3)) * q.ldo, 0);
+      for (int r4 = 0; r4 < 4; ++r4) {
+        GateTile dh, dg, du;
+        if (hlines) unpack_piece(w[i][r4], pl.sel, dh);
+        else load_piece(dh, i, r4, pl, cols, q.lddh, q.dh_bf16, rh);
+        if (q.p.act == 0) gate_piece_backward_act<0>(q.p, acc, i, r4, dh, dg, du);
+        else if (q.p.act == 1) gate_piece_backward_act<1>(q.p, acc, i, r4, dh, dg, du);
+        else gate_piece_backward_act<2>(q.p, acc, i, r4, dh, dg, du);
+        if constexpr (BMAP == t256c::B_HALVES) {
+          if (lines) {
+            store_piece_lines(dg, i, r4, pl, voff, q.ldo, rg);
+            store_piece_lines(du, i, r4, pl, voff, q.ldo, ru);
           } else {
-            store_block(g[j], i, 2 * col, live, q.ldo, q.out_bf16, rg);
-            store_block(u[j], i, 2 * col + 1, live, q.ldo, q.out_bf16, rg);
+            store_piece(dg, i, r4, pl, 1, 0, cols, q.ldo, q.out_bf16, rg);
+            store_piece(du, i, r4, pl, 1, 0, cols, q.ldo, q.out_bf16, ru);
           }
+        } else if (even) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int c = pl.col + 32 * j;
+            const uint32_t vo = c < cols ? (uint32_t)(2 * (pl.row * q.ldo + 2 * c)) : OOB;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              __builtin_amdgcn_raw_buffer_store_b32(
+                  (uint32_t)__builtin_bit_cast(unsigned short, (__bf16)dg.t[j][k]) |
+                      ((uint32_t)__builtin_bit_cast(unsigned short, (__bf16)du.t[j][k]) << 16),
+                  rg, vo, 2 * (32 * i + 8 * r4 + k) * q.ldo, 0);
+          }
+        } else {
+          store_piece(dg, i, r4, pl, 2, 0, cols, q.ldo, q.out_bf16, rg);
+          store_piece(du, i, r4, pl, 2, 1, cols, q.ldo, q.out_bf16, rg);
         }
       }
-      if constexpr (BMAP == t256c::B_HALVES) {
-        const bool lines = even && (cols & 1) == 0 && (N & 1) == 0;
-        store_halves(g[0], g[1], i, q.ldo, cols, q.out_bf16, lines, rg);
-        store_halves(u[0], u[1], i, q.ldo, cols, q.out_bf16, lines, ru);
-      }
-    }
   }
 }
 #endif

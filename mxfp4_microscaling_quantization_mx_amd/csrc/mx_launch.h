@@ -240,5 +240,8 @@ hipError_t launch_gated(const GatedArgs& a, hipStream_t st);
 // takes this problem's types and layout, and its launch.
 bool gated256_layout_ok(const GatedArgs& a);
 hipError_t launch_gated256(const GatedArgs& a, hipStream_t st);
+// The same on the MXFP8 / MXFP6 pipeline (gated_f8.hip).
+bool gated_f8_layout_ok(const GatedArgs& a);
+hipError_t launch_gated_f8(const GatedArgs& a, hipStream_t st);
 
 }  // namespace mx
