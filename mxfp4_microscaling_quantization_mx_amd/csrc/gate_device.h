@@ -25,10 +25,16 @@ namespace mx {
 struct GateP {
   int act;
   float alpha, limit, shift;     // limit +inf: no clamp
+  float alpha_log2e;             // alpha log2 e, rounded once
 };
 
-__device__ __forceinline__ float gate_sigmoid(float z) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+inline GateP gate_params(int act, float alpha, float limit, float shift) {
+  return GateP{act, alpha, limit, shift, (float)((double)alpha * 1.4426950408889634)};
+}
+
+// 1 / (1 + 2^-y)
+__device__ __forceinline__ float gate_sigmoid2(float y) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-y));
 }
 
 // act(x) for the mx_act value ACT, and with GRAD its derivative in d.
@@ -48,41 +54,41 @@ __device__ __forceinline__ float gate_act(const GateP& p, float x, float& d) {
     if (GRAD) d = __builtin_fmaf(x * 0.39894228040143268f, e, cdf);
     return x * cdf;
   } else {
-    float z, dz;
+    float s, dz;
     if constexpr (ACT == 2) {                            // GELU, tanh form
       // s is exactly 0 or 1 well inside |x| = 16, so the polynomial may stop
       // there; NaN stays in the factor x
       const float c = __builtin_amdgcn_fmed3f(x, -16.0f, 16.0f), c2 = c * c;
-      z = 1.59576912160573071f * __builtin_fmaf(0.044715f * c2, c, c);
-      dz = 1.59576912160573071f * __builtin_fmaf(0.134145f, c2, 1.0f);
+      s = gate_sigmoid2(c * __builtin_fmaf(0.10294324f, c2, 2.30220818f));   // z log2 e
+      dz = __builtin_fmaf(0.21406498f, c2, 1.59576912f);
     } else {                                             // SiLU
-      z = p.alpha * x;
+      s = gate_sigmoid2(p.alpha_log2e * x);
       dz = p.alpha;
     }
-    const float s = gate_sigmoid(z);
-    if (GRAD) d = __builtin_fmaf(x, s * (1.0f - s) * dz, s);
-    return x * s;
+    const float a = x * s;
+    if (GRAD) d = __builtin_fmaf(a, (1.0f - s) * dz, s);
+    return a;
   }
 }
 
-// (the comparisons keep NaN)
+// Clamps that keep NaN (V_MINIMUM3_F32, V_MAXIMUM3_F32).
+__device__ __forceinline__ float gate_low(float x, float lim) { return __builtin_elementwise_minimum(x, lim); }
+__device__ __forceinline__ float gate_clamp(float x, float lim) {
+  return __builtin_elementwise_minimum(__builtin_elementwise_maximum(x, -lim), lim);
+}
+
 template <int ACT>
 __device__ __forceinline__ float gate_forward(const GateP& p, float g, float u) {
-  const float gc = g > p.limit ? p.limit : g;
-  const float uc = u > p.limit ? p.limit : u < -p.limit ? -p.limit : u;
   float d;
-  return gate_act<ACT, false>(p, gc, d) * (uc + p.shift);
+  return gate_act<ACT, false>(p, gate_low(g, p.limit), d) * (gate_clamp(u, p.limit) + p.shift);
 }
 
 template <int ACT>
 __device__ __forceinline__ void gate_backward(const GateP& p, float g, float u, float dh, float& dg, float& du) {
-  const float gc = g > p.limit ? p.limit : g;
-  const bool hi = u > p.limit, lo = u < -p.limit;
-  const float uc = hi ? p.limit : lo ? -p.limit : u;
   float d;
-  const float a = gate_act<ACT, true>(p, gc, d);
-  dg = g > p.limit ? 0.0f : dh * (uc + p.shift) * d;
-  du = hi || lo ? 0.0f : dh * a;
+  const float a = gate_act<ACT, true>(p, gate_low(g, p.limit), d);
+  dg = g > p.limit ? 0.0f : dh * (gate_clamp(u, p.limit) + p.shift) * d;
+  du = __builtin_fabsf(u) > p.limit ? 0.0f : dh * a;
 }
 
 // The same with the activation chosen at run time.

@@ -74,7 +74,7 @@ hipError_t launch_gated256(const GatedArgs& a, hipStream_t st) {
   const int64_t tiles_m = a.offsets ? (a.M + 255) / 256 + a.E : (a.M + 255) / 256;
   const int64_t tiles = tiles_m * tiles_n;
   const unsigned nwg = (unsigned)(tiles < cus ? tiles : cus);
-  const t256c::GateOut go{GateP{a.act, a.alpha, a.limit, a.up_shift}, a.out, a.dH, (int)a.ldo, (int)a.lddh,
+  const t256c::GateOut go{gate_params(a.act, a.alpha, a.limit, a.up_shift), a.out, a.dH, (int)a.ldo, (int)a.lddh,
                           (int)a.out_bf16, (int)a.dh_bf16};
 #define MX_GT(A_, B_, L_, D_)                                                                                       \
   do {                                                                                                              \

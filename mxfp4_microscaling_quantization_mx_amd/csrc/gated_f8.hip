@@ -64,7 +64,7 @@ hipError_t launch_f8(const GatedArgs& a, hipStream_t st) {
   const int64_t tiles_m = a.offsets ? (a.M + 255) / 256 + a.E : (a.M + 255) / 256;
   const int64_t tiles = tiles_m * tiles_n;
   const unsigned nwg = (unsigned)(tiles < cus ? tiles : cus);
-  const t256c::GateOut go{GateP{a.act, a.alpha, a.limit, a.up_shift}, a.out, a.dH, (int)a.ldo, (int)a.lddh,
+  const t256c::GateOut go{gate_params(a.act, a.alpha, a.limit, a.up_shift), a.out, a.dH, (int)a.ldo, (int)a.lddh,
                           (int)a.out_bf16, (int)a.dh_bf16};
   if (a.offsets)
     hipLaunchKernelGGL((k_grouped_gated_f8<FA, FB>), dim3(nwg), dim3(512), 0, st, a.A, a.B, a.M, (int)a.N, (int)a.K,

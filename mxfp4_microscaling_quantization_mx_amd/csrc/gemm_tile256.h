@@ -113,25 +113,26 @@ struct alignas(16) GateOut {
   int ldo, lddh;
   int out_bf16, dh_bf16;
 };
-static_assert(sizeof(GateOut) == 48, "three 16-byte LDS reads");
+static_assert(sizeof(GateOut) == 64, "four 16-byte LDS reads");
 
 // A wave-uniform GateOut kept in LDS, read with one wait (in scalar registers
 // across the pipeline it would spill).
 __device__ __forceinline__ GateOut load_gate_out(const GateOut* p) {
   typedef int v4 __attribute__((ext_vector_type(4)));
-  v4 q[3];
+  v4 q[4];
   const uint32_t a = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
   asm volatile(
-      "ds_read_b128 %0, %3\n\t"
-      "ds_read_b128 %1, %3 offset:16\n\t"
-      "ds_read_b128 %2, %3 offset:32\n\t"
+      "ds_read_b128 %0, %4\n\t"
+      "ds_read_b128 %1, %4 offset:16\n\t"
+      "ds_read_b128 %2, %4 offset:32\n\t"
+      "ds_read_b128 %3, %4 offset:48\n\t"
       "s_waitcnt lgkmcnt(0)"
-      : "=&v"(q[0]), "=&v"(q[1]), "=&v"(q[2])
+      : "=&v"(q[0]), "=&v"(q[1]), "=&v"(q[2]), "=&v"(q[3])
       : "v"(a)
       : "memory");
-  int w[12];
+  int w[16];
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[4 * i + k] = __builtin_amdgcn_readfirstlane(q[i][k]);
   return __builtin_bit_cast(GateOut, w);
@@ -1101,7 +1102,7 @@ __device__ __forceinline__ void store_unit(Acc& acc, const Sched& sc, int j, voi
 // allows it: h, dH, and dg and du of the halves order through the exchanges
 // of store_bf16_rows (which undo themselves); interleaved, a lane's dg and du
 // are neighbours, so one 4-byte store per lane writes the 32 pairs of two
-// rows.  The 32 words of dH are all requested before the first is used.
+// rows.  The words of a row tile's dH are all requested before the first is used.
 struct GateTile {
   float t[2][4];                           // column tile, row 4 kh + q
 };
@@ -1256,18 +1257,7 @@ __device__ __forceinline__ void store_tile_gate(const Acc& acc, const t256c::Gat
     const int N = n0 + nlim, eh = q.dh_bf16 ? 2 : 4;
     const __amdgpu_buffer_rsrc_t rh = block_rsrc(q.dH, row0, n0, q.lddh, rows, cols, eh);
     const bool hlines = q.dh_bf16 && ((q.lddh | cols) & 1) == 0 && ((uintptr_t)q.dH & 3) == 0;
-    uint32_t w[TI][4][4];
-    if (hlines) {
-      const uint32_t vo = line_in ? (uint32_t)((pl.line_row * q.lddh + pl.line_col) * 2) : OOB;
-#pragma unroll
-      for (int i = 0; i < TI; ++i)
-#pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            w[i][r4][k] = __builtin_amdgcn_raw_buffer_load_b32(
-                rh, vo, 2 * (32 * i + 8 * r4 + (k & 2) + 4 * (k & 1)) * q.lddh, 0);
-    }
+    const uint32_t hoff = line_in ? (uint32_t)((pl.line_row * q.lddh + pl.line_col) * 2) : OOB;
     // dg's columns and, interleaved, du's between them; as halves, du's are N further
     const __amdgpu_buffer_rsrc_t rg = BMAP == t256c::B_HALVES
                                           ? block_rsrc(q.out, row0, n0, q.ldo, rows, cols, eo)
@@ -1276,11 +1266,18 @@ __device__ __forceinline__ void store_tile_gate(const Acc& acc, const t256c::Gat
     const bool lines = even && (cols & 1) == 0 && (N & 1) == 0;
     const uint32_t voff = line_in ? (uint32_t)((pl.line_row * q.ldo + pl.line_col) * 2) : OOB;
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+    for (int i = 0; i < TI; ++i) {
+      uint32_t w[2][4];
 #pragma unroll
       for (int r4 = 0; r4 < 4; ++r4) {
+        if (hlines && (r4 & 1) == 0) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            w[k >> 2][k & 3] = __builtin_amdgcn_raw_buffer_load_b32(
+                rh, hoff, 2 * (32 * i + 8 * (r4 + (k >> 2)) + (k & 2) + 4 * (k & 1)) * q.lddh, 0);
+        }
         GateTile dh, dg, du;
-        if (hlines) unpack_piece(w[i][r4], pl.sel, dh);
+        if (hlines) unpack_piece(w[r4 & 1], pl.sel, dh);
         else load_piece(dh, i, r4, pl, cols, q.lddh, q.dh_bf16, rh);
         if (q.p.act == 0) gate_piece_backward_act<0>(q.p, acc, i, r4, dh, dg, du);
         else if (q.p.act == 1) gate_piece_backward_act<1>(q.p, acc, i, r4, dh, dg, du);
@@ -1310,6 +1307,7 @@ __device__ __forceinline__ void store_tile_gate(const Acc& acc, const t256c::Gat
           store_piece(du, i, r4, pl, 2, 1, cols, q.ldo, q.out_bf16, rg);
         }
       }
+    }
   }
 }
 #endif
