@@ -134,7 +134,9 @@ def _check(status):
 
 
 def _stream(t):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    # the handle of torch.cuda.current_stream(t.device), without building the
+    # Stream object (2 us of a 4 us launch)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(t.get_device()))
 
 
 def _ptr(t):
@@ -443,11 +445,15 @@ class Gate:
                         0.0 if self.limit is None else self.limit, self.up_shift)
 
 
-def _check_rows(t, shape, what):
-    if t.dim() != 2 or tuple(t.shape) != tuple(shape) or t.dtype not in _DTYPE or not t.is_cuda:
-        raise ValueError(f"{what} must be a bf16/float32 CUDA tensor of shape {tuple(shape)}")
+def _check_rows(t, what, shape=None, dtype=None):
+    if t.dim() != 2 or t.dtype not in _DTYPE or not t.is_cuda:
+        raise ValueError(f"{what} must be a 2-D bf16/float32 CUDA tensor")
     if t.stride(1) != 1 and t.shape[1] > 1:
         raise ValueError(f"{what} must be row-major (stride(1) == 1)")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}")
 
 
 def _gated(what, a, b, gate, out, out_dtype, dh, offsets):
@@ -466,12 +472,12 @@ def _gated(what, a, b, gate, out, out_dtype, dh, offsets):
     N = rows // 2
     shape = (a.rows, rows if backward else N)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=a.codes.device)
+        out = a.codes.new_empty(shape, dtype=out_dtype)
     else:
-        _check_rows(out, shape, f"{what}: out")
+        _check_rows(out, f"{what}: out", shape)
     args = ()
     if backward:
-        _check_rows(dh, (a.rows, N), f"{what}: dh")
+        _check_rows(dh, f"{what}: dh", (a.rows, N))
         args = (_ptr(dh), _DTYPE[dh.dtype], dh.stride(0))
     at, gc = a.c_struct(), gate.c_struct()
     _check(getattr(lib, what)(ctypes.byref(at), *group, ctypes.byref(gc), *args, _ptr(out), _DTYPE[out.dtype],
@@ -517,24 +523,22 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None):
     mx_layer_norm): (y, mean, rstd), the row statistics in float32 for
     layer_norm_backward."""
     lib = load_library()
-    _check_rows(x, x.shape, "layer_norm: x")
+    _check_rows(x, "layer_norm: x")
     R, C = x.shape
     if weight is not None:
         _norm_param(weight, C, None, "layer_norm: weight")
     if bias is not None:
         _norm_param(bias, C, None if weight is None else weight.dtype, "layer_norm: bias")
     if out is None:
-        out = torch.empty((R, C), dtype=x.dtype, device=x.device)
+        out = x.new_empty((R, C))
     else:
-        _check_rows(out, x.shape, "layer_norm: out")
-        if out.dtype != x.dtype:
-            raise ValueError("layer_norm: out must have x's dtype")
-    stats = torch.empty((2, R), dtype=torch.float32, device=x.device)
+        _check_rows(out, "layer_norm: out", x.shape, x.dtype)
+    mean, rstd = x.new_empty(R, dtype=torch.float32), x.new_empty(R, dtype=torch.float32)
     wd = weight if weight is not None else bias
     _check(lib.mx_layer_norm(_ptr(x), _DTYPE[x.dtype], R, C, x.stride(0), _ptr(weight), _ptr(bias),
                              MX_DT_F32 if wd is None else _DTYPE[wd.dtype], eps, _ptr(out), out.stride(0),
-                             _ptr(stats[0]), _ptr(stats[1]), _stream(x)))
-    return out, stats[0], stats[1]
+                             _ptr(mean), _ptr(rstd), _stream(x)))
+    return out, mean, rstd
 
 
 def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, param_dtype=None):
@@ -542,30 +546,28 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, param_dtype=No
     mx_layer_norm_backward).  dweight and dbias have the weight's dtype, or
     param_dtype without one (default float32); out receives dx."""
     lib = load_library()
-    _check_rows(x, x.shape, "layer_norm_backward: x")
-    _check_rows(dy, x.shape, "layer_norm_backward: dy")
-    if dy.dtype != x.dtype:
-        raise ValueError("layer_norm_backward: dy must have x's dtype")
+    _check_rows(x, "layer_norm_backward: x")
+    _check_rows(dy, "layer_norm_backward: dy", x.shape, x.dtype)
     R, C = x.shape
     for t, n in ((mean, "mean"), (rstd, "rstd")):
-        if t.shape != (R,) or t.dtype != torch.float32 or not t.is_cuda or (t.stride(0) != 1 and R > 1):
+        if t.shape != (R,) or t.dtype != torch.float32 or not t.is_cuda or (R > 1 and t.stride(0) != 1):
             raise ValueError(f"layer_norm_backward: {n} must be a contiguous float32 CUDA tensor of {R} entries")
     if weight is not None:
         _norm_param(weight, C, param_dtype, "layer_norm_backward: weight")
         param_dtype = weight.dtype
+    elif param_dtype is None:
+        param_dtype = torch.float32
     if out is None:
-        out = torch.empty((R, C), dtype=x.dtype, device=x.device)
+        out = x.new_empty((R, C))
     else:
-        _check_rows(out, x.shape, "layer_norm_backward: out")
-        if out.dtype != x.dtype:
-            raise ValueError("layer_norm_backward: out must have x's dtype")
-    grads = torch.empty((2, C), dtype=param_dtype or torch.float32, device=x.device)
+        _check_rows(out, "layer_norm_backward: out", x.shape, x.dtype)
+    dweight, dbias = x.new_empty(C, dtype=param_dtype), x.new_empty(C, dtype=param_dtype)
     nbytes = lib.mx_layer_norm_backward_workspace_size(R, C)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    ws = x.new_empty(nbytes, dtype=torch.uint8)
     _check(lib.mx_layer_norm_backward(_ptr(dy), _ptr(x), _DTYPE[x.dtype], R, C, dy.stride(0), x.stride(0), _ptr(mean),
-                                      _ptr(rstd), _ptr(weight), _DTYPE[grads.dtype], _ptr(out), out.stride(0),
-                                      _ptr(grads[0]), _ptr(grads[1]), _ptr(ws), nbytes, _stream(x)))
-    return out, grads[0], grads[1]
+                                      _ptr(rstd), _ptr(weight), _DTYPE[param_dtype], _ptr(out), out.stride(0),
+                                      _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes, _stream(x)))
+    return out, dweight, dbias
 
 
 def dropout(x, p, seed=0, offset=0, residual=None, out=None):
@@ -573,18 +575,18 @@ def dropout(x, p, seed=0, offset=0, residual=None, out=None):
     optional residual (see mx_dropout).  The backward pass is this call on the
     gradient with the same p, seed and offset and no residual."""
     lib = load_library()
-    _check_rows(x, x.shape, "dropout: x")
-    for t, n in ((residual, "residual"), (out, "out")):
-        if t is not None:
-            _check_rows(t, x.shape, f"dropout: {n}")
-            if t.dtype != x.dtype:
-                raise ValueError(f"dropout: {n} must have x's dtype")
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _check_rows(x, "dropout: x")
     R, C = x.shape
+    ldr = 0
+    if residual is not None:
+        _check_rows(residual, "dropout: residual", x.shape, x.dtype)
+        ldr = residual.stride(0)
+    if out is None:
+        out = x.new_empty((R, C))
+    else:
+        _check_rows(out, "dropout: out", x.shape, x.dtype)
     _check(lib.mx_dropout(_ptr(x), _DTYPE[x.dtype], R, C, x.stride(0), p, seed & (2**64 - 1), offset & (2**64 - 1),
-                          _ptr(residual), 0 if residual is None else residual.stride(0), _ptr(out), out.stride(0),
-                          _stream(x)))
+                          _ptr(residual), ldr, _ptr(out), out.stride(0), _stream(x)))
     return out
 
 
