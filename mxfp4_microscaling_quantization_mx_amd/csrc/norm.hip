@@ -9,14 +9,19 @@
 // values (a difference of sums would cancel where |mean| >> the spread).
 //
 // Both directions are bound by HBM bandwidth (bf16: 4 bytes per element
-// forward, 6 backward), so a row is read once and held in registers:
+// forward, 6 backward; a device copy reaches 5.1 TB/s), so a row is read once
+// and held in registers:
 //  * k_norm: 1, 4 or 16 waves per row, each lane VEC consecutive elements (16
 //    bytes where the rows allow it, else single elements) of every NV-th
-//    piece of the row.
-//  * k_norm_backward: 1 to 8 waves per row, workgroups of 8 waves walking the
-//    rows; each lane also keeps the sums of dw and db of its columns in
-//    registers over all its rows, adds them over the workgroup's row groups
-//    through LDS at the end and stores one partial row [2][C] per workgroup.
+//    piece of the row.  16384 x 2880 bf16: 37 us, 5.1 TB/s.
+//  * k_norm_backward: 1 to 8 waves per row, as few as leave a lane about 24
+//    elements; workgroups of 8 waves walk the rows, one per CU (two lost 10 %
+//    to the doubled partial rows).  Each lane keeps its weights and its sums
+//    of dw and db in registers and requests a row while the one before is
+//    worked on; the workgroup's row groups are added through LDS at the end
+//    and stored as one partial row [2][C].  16384 x 2880 bf16: 51 us, 5.6 TB/s
+//    (72 us with one wave per row, the weights read again and no row ahead);
+//    4099 x 1111 float32, unaligned: 16 us, 3.4 TB/s.
 //  * k_norm_any, k_norm_dx_any, k_norm_dw_any: rows too long for registers,
 //    read once per sum (the later reads come from cache), the weight's
 //    gradient by columns.
@@ -312,70 +317,87 @@ __device__ __forceinline__ void group_sum2(float& p, float& q, float2 (*red)[BW]
   }
 }
 
+// Each wave holds its columns of the weight and its sums of dw and db over all
+// its rows, and requests a row's x and dy while the row before it is worked on.
 template <bool BF16, int VEC, int NV, int WPR>
 __global__ __launch_bounds__(64 * BW) void k_norm_backward(NormBwdArgs a) {
   constexpr int RPB = BW / WPR, RL = 64 * WPR;  // row groups, lanes per row
+  constexpr int ES = BF16 ? 2 : 4;
+  constexpr int S = NV < 8 / VEC ? NV : 8 / VEC > 0 ? 8 / VEC : 1;   // pieces per LDS exchange at the end
   __shared__ float2 red[2][BW];
-  __shared__ float part[2][RPB][RL * VEC];
+  __shared__ float part[2][RPB][RL * VEC * S];
   const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / RL);
   const uint32_t t = threadIdx.x % RL, C = (uint32_t)a.C;
-  constexpr int ES = BF16 ? 2 : 4;
   const float inv = 1.0f / (float)a.C;
-  float dw[NV * VEC], db[NV * VEC];
+  float w[NV * VEC], dw[NV * VEC], db[NV * VEC];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const uint32_t c = (v * RL + t) * VEC;
+    load_param<VEC>(c < C ? a.weight : nullptr, a.w_bf16, c, 1.0f, w + v * VEC);
+  }
 #pragma unroll
   for (int k = 0; k < NV * VEC; ++k) dw[k] = db[k] = 0.0f;
-  int turn = 0;
-  // every wave of the workgroup makes the same number of passes (they share
-  // the barriers); a row group past the last row adds nothing
-  for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.R; base += (int64_t)gridDim.x * RPB, turn ^= 1) {
-    const int64_t r = base + sub;
-    const bool row = r < a.R;
-    const float mean = row ? a.mean[r] : 0.0f, rstd = row ? a.rstd[r] : 0.0f;
-    const char* const xr = static_cast<const char*>(a.x) + r * a.ldx * ES;
-    const char* const gr = static_cast<const char*>(a.dy) + r * a.lddy * ES;
-    char* const dr = static_cast<char*>(a.dx) + r * a.lddx * ES;
+  struct Row {
     Vec<BF16, VEC> x[NV], g[NV];
+    float mean, rstd;
+  };
+  // a row group past the last row reads zeros, with mean = rstd = 0
+  auto load = [&](Row& o, int64_t r) {
+    const bool row = r < a.R;
+    const int64_t at = row ? r : 0;
+    o.mean = row ? a.mean[at] : 0.0f;
+    o.rstd = row ? a.rstd[at] : 0.0f;
+    const char* const xr = static_cast<const char*>(a.x) + at * a.ldx * ES;
+    const char* const gr = static_cast<const char*>(a.dy) + at * a.lddy * ES;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const uint32_t c = (v * RL + t) * VEC;
       if (row && c < C) {
-        x[v].load(xr, c);
-        g[v].load(gr, c);
+        o.x[v].load(xr, c);
+        o.g[v].load(gr, c);
       } else {
-        x[v].zero();
-        g[v].zero();
+        o.x[v].zero();
+        o.g[v].zero();
       }
     }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t base = (int64_t)blockIdx.x * RPB;
+  Row next;
+  load(next, base + sub);
+  // every wave of the workgroup makes the same number of passes (they share
+  // the barriers)
+  for (int turn = 0; base < a.R; base += step, turn ^= 1) {
+    const Row cur = next;
+    const int64_t r = base + sub;
+    if (base + step < a.R) load(next, r + step);
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const uint32_t c = (v * RL + t) * VEC;
-      float w[VEC];
-      load_param<VEC>(c < C ? a.weight : nullptr, a.w_bf16, c, 1.0f, w);
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
-        const float dy = g[v].get(k), xh = (x[v].get(k) - mean) * rstd, gy = dy * w[k];
+        const int e = v * VEC + k;
+        const float dy = cur.g[v].get(k), xh = (cur.x[v].get(k) - cur.mean) * cur.rstd, gy = dy * w[e];
         s1 = s1 + gy;
         s2 = __builtin_fmaf(gy, xh, s2);
         // a row past the end has dy = 0 and xh = 0; a column past it is not stored
-        dw[v * VEC + k] = __builtin_fmaf(dy, xh, dw[v * VEC + k]);
-        db[v * VEC + k] = db[v * VEC + k] + dy;
+        dw[e] = __builtin_fmaf(dy, xh, dw[e]);
+        db[e] = db[e] + dy;
       }
-    }
     group_sum2<WPR>(s1, s2, red, turn);
-    if (a.dx && row) {
+    if (a.dx && r < a.R) {
       s1 = s1 * inv;
       s2 = s2 * inv;
+      char* const dr = static_cast<char*>(a.dx) + r * a.lddx * ES;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const uint32_t c = (v * RL + t) * VEC;
         if (c < C) {
-          float w[VEC], o[VEC];
-          load_param<VEC>(a.weight, a.w_bf16, c, 1.0f, w);
+          float o[VEC];
 #pragma unroll
           for (int k = 0; k < VEC; ++k) {
-            const float xh = (x[v].get(k) - mean) * rstd;
-            o[k] = rstd * ((g[v].get(k) * w[k] - s1) - xh * s2);
+            const float xh = (cur.x[v].get(k) - cur.mean) * cur.rstd;
+            o[k] = cur.rstd * ((cur.g[v].get(k) * w[v * VEC + k] - s1) - xh * s2);
           }
           Vec<BF16, VEC>::store(dr, c, o);
         }
@@ -383,21 +405,33 @@ __global__ __launch_bounds__(64 * BW) void k_norm_backward(NormBwdArgs a) {
     }
   }
   if (!a.workspace) return;
+  // the row groups' sums, S pieces at a time, added in group order; a launch
+  // of one workgroup writes the results themselves
+  const bool last = gridDim.x == 1;
   float* const out = a.workspace + (int64_t)blockIdx.x * 2 * a.C;
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
+  for (int v0 = 0; v0 < NV; v0 += S) {
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      part[0][sub][t * VEC + k] = dw[v * VEC + k];
-      part[1][sub][t * VEC + k] = db[v * VEC + k];
-    }
+    for (int v = v0; v < v0 + S && v < NV; ++v)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        part[0][sub][((v - v0) * RL + t) * VEC + k] = dw[v * VEC + k];
+        part[1][sub][((v - v0) * RL + t) * VEC + k] = db[v * VEC + k];
+      }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * RL * VEC; i += 64 * BW) {
-      const int which = i / (RL * VEC), j = i - which * RL * VEC, c = v * RL * VEC + j;
+    constexpr int LEN = RL * VEC * S;
+    for (int i = threadIdx.x; i < 2 * LEN; i += 64 * BW) {
+      const int which = i / LEN, j = i - which * LEN, c = v0 * RL * VEC + j;
+      if (c >= a.C || j >= (NV - v0) * RL * VEC) continue;
       float s = part[which][0][j];
 #pragma unroll
       for (int q = 1; q < RPB; ++q) s = s + part[which][q][j];
-      if (c < a.C) out[(int64_t)which * a.C + c] = s;
+      if (!last) {
+        out[(int64_t)which * a.C + c] = s;
+      } else if (void* const d = which ? a.dbias : a.dweight) {
+        if (a.w_bf16) st1<true>(d, c, s);
+        else st1<false>(d, c, s);
+      }
     }
     __syncthreads();
   }
@@ -413,8 +447,18 @@ __global__ __launch_bounds__(1024) void k_norm_dw_sum(const float* __restrict__ 
   void* const out = blockIdx.y ? dbias : dweight;
   if (!out) return;
   float s = 0.0f;
-  if (c < C)
-    for (int g = w; g < G; g += 16) s = s + part[((int64_t)g * 2 + blockIdx.y) * C + c];
+  if (c < C) {
+    const float* const p = part + (int64_t)blockIdx.y * C + c;
+    int g = w;
+    for (; g + 7 * 16 < G; g += 8 * 16) {       // eight loads in flight
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = p[(int64_t)(g + 16 * k) * 2 * C];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s = s + v[k];
+    }
+    for (; g < G; g += 16) s = s + p[(int64_t)g * 2 * C];
+  }
   red[w][lane] = s;
   __syncthreads();
   if (w == 0 && c < C) {
@@ -425,8 +469,8 @@ __global__ __launch_bounds__(1024) void k_norm_dw_sum(const float* __restrict__ 
   }
 }
 
-// Partial rows of dw and db: workgroups of k_norm_backward (one per CU: its
-// registers allow no more) and row groups of k_norm_dw_any.
+// Partial rows of dw and db: workgroups of k_norm_backward (one per CU) and row
+// groups of k_norm_dw_any.
 constexpr int64_t MOST_GROUPS = 256;
 int64_t norm_groups(int64_t R) { return R < MOST_GROUPS ? R : MOST_GROUPS; }
 
@@ -486,20 +530,19 @@ template <bool BF16, int VEC>
 int64_t try_norm_backward(const NormBwdArgs& a, hipStream_t st) {
   if constexpr (VEC == 8) {
     MX_NV(start_norm_backward, 1, 1) MX_NV(start_norm_backward, 2, 1) MX_NV(start_norm_backward, 3, 1)
-    MX_NV(start_norm_backward, 4, 1) MX_NV(start_norm_backward, 5, 1) MX_NV(start_norm_backward, 6, 1)
-    MX_NV(start_norm_backward, 4, 2) MX_NV(start_norm_backward, 5, 2) MX_NV(start_norm_backward, 6, 2)
-    MX_NV(start_norm_backward, 4, 4) MX_NV(start_norm_backward, 6, 4) MX_NV(start_norm_backward, 4, 8)
-    MX_NV(start_norm_backward, 6, 8)
+    MX_NV(start_norm_backward, 2, 2) MX_NV(start_norm_backward, 3, 2) MX_NV(start_norm_backward, 2, 4)
+    MX_NV(start_norm_backward, 3, 4) MX_NV(start_norm_backward, 2, 8) MX_NV(start_norm_backward, 3, 8)
+    MX_NV(start_norm_backward, 4, 8)
   } else if constexpr (VEC == 4) {
     MX_NV(start_norm_backward, 1, 1) MX_NV(start_norm_backward, 2, 1) MX_NV(start_norm_backward, 4, 1)
-    MX_NV(start_norm_backward, 6, 1) MX_NV(start_norm_backward, 8, 1)
-    MX_NV(start_norm_backward, 6, 2) MX_NV(start_norm_backward, 8, 2) MX_NV(start_norm_backward, 6, 4)
-    MX_NV(start_norm_backward, 8, 4) MX_NV(start_norm_backward, 6, 8) MX_NV(start_norm_backward, 8, 8)
+    MX_NV(start_norm_backward, 3, 2) MX_NV(start_norm_backward, 4, 2) MX_NV(start_norm_backward, 3, 4)
+    MX_NV(start_norm_backward, 4, 4) MX_NV(start_norm_backward, 3, 8) MX_NV(start_norm_backward, 4, 8)
+    MX_NV(start_norm_backward, 6, 8)
   } else {
     MX_NV(start_norm_backward, 2, 1) MX_NV(start_norm_backward, 4, 1) MX_NV(start_norm_backward, 8, 1)
-    MX_NV(start_norm_backward, 12, 1) MX_NV(start_norm_backward, 18, 1) MX_NV(start_norm_backward, 24, 1)
-    MX_NV(start_norm_backward, 18, 2) MX_NV(start_norm_backward, 24, 2) MX_NV(start_norm_backward, 18, 4)
-    MX_NV(start_norm_backward, 24, 4) MX_NV(start_norm_backward, 18, 8) MX_NV(start_norm_backward, 24, 8)
+    MX_NV(start_norm_backward, 12, 1) MX_NV(start_norm_backward, 18, 1) MX_NV(start_norm_backward, 12, 2)
+    MX_NV(start_norm_backward, 18, 2) MX_NV(start_norm_backward, 12, 4) MX_NV(start_norm_backward, 18, 4)
+    MX_NV(start_norm_backward, 12, 8) MX_NV(start_norm_backward, 18, 8)
   }
   return 0;
 }
@@ -533,6 +576,7 @@ hipError_t launch_layer_norm_backward(const NormBwdArgs& args, hipStream_t st) {
     const bool vec = norm_vec(a.C, a.bf16, {a.ldx, a.lddy, a.dx ? a.lddx : 0}, {a.x, a.dy, a.dx, a.weight});
     G = a.bf16 ? (vec ? try_norm_backward<true, 8>(a, st) : try_norm_backward<true, 1>(a, st))
                : (vec ? try_norm_backward<false, 4>(a, st) : try_norm_backward<false, 1>(a, st));
+    if (G == 1) return hipGetLastError();             // (its one workgroup wrote them)
     if (G == 0) {
       // the weight's gradients first: dx may be written over dy or x
       if (sums) {
