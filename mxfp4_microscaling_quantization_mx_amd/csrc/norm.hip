@@ -11,17 +11,19 @@
 // Both directions are bound by HBM bandwidth (bf16: 4 bytes per element
 // forward, 6 backward; a device copy reaches 5.1 TB/s), so a row is read once
 // and held in registers:
-//  * k_norm: 1, 4 or 16 waves per row, each lane VEC consecutive elements (16
-//    bytes where the rows allow it, else single elements) of every NV-th
-//    piece of the row.  16384 x 2880 bf16: 37 us, 5.1 TB/s.
-//  * k_norm_backward: 1 to 8 waves per row, as few as leave a lane about 24
-//    elements; workgroups of 8 waves walk the rows, one per CU (two lost 10 %
-//    to the doubled partial rows).  Each lane keeps its weights and its sums
-//    of dw and db in registers and requests a row while the one before is
-//    worked on; the workgroup's row groups are added through LDS at the end
-//    and stored as one partial row [2][C].  16384 x 2880 bf16: 51 us, 5.6 TB/s
-//    (72 us with one wave per row, the weights read again and no row ahead);
-//    4099 x 1111 float32, unaligned: 16 us, 3.4 TB/s.
+//  * k_norm: 1 to 8 waves per row, as few as leave a lane about 24 elements:
+//    VEC consecutive ones (16 bytes where the rows allow it, else single
+//    elements) of every NV-th piece of the row.  Workgroups of 8 waves walk
+//    the rows; each lane keeps its weights in registers and requests a row
+//    while the one before is worked on.  16384 x 2880 bf16: 34-38 us, 5.0-5.6
+//    TB/s (44 us with one row per wave, whose weights came through L2 each
+//    time).
+//  * k_norm_backward: the same, one workgroup per CU (two lost 10 % to the
+//    doubled partial rows), each lane also keeping its sums of dw and db; the
+//    workgroup's row groups are added through LDS at the end and stored as one
+//    partial row [2][C].  16384 x 2880 bf16: 51 us, 5.6 TB/s (72 us with one
+//    wave per row, the weights read again and no row ahead); 4099 x 1111
+//    float32, unaligned: 16 us, 3.5 TB/s.
 //  * k_norm_any, k_norm_dx_any, k_norm_dw_any: rows too long for registers,
 //    read once per sum (the later reads come from cache), the weight's
 //    gradient by columns.
@@ -235,65 +237,7 @@ __device__ __forceinline__ void load_param(const void* p, bool bf16, uint32_t c,
   }
 }
 
-template <int WPR>
-constexpr int norm_threads() { return WPR > 4 ? 64 * WPR : 256; }
-
-template <bool BF16, int VEC, int NV, int WPR>
-__global__ __launch_bounds__(norm_threads<WPR>()) void k_norm(NormArgs a) {
-  constexpr int TH = norm_threads<WPR>(), RPB = TH / (64 * WPR);
-  static_assert(WPR == 1 || RPB == 1, "a row's waves are the workgroup, or one wave");
-  __shared__ float red[TH / 64];
-  const int sub = WPR == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
-  const uint32_t t = WPR == 1 ? threadIdx.x & 63 : threadIdx.x, C = (uint32_t)a.C;
-  constexpr int ES = BF16 ? 2 : 4;
-  for (int64_t r = (int64_t)blockIdx.x * RPB + sub; r < a.R; r += (int64_t)gridDim.x * RPB) {
-    const char* const xr = static_cast<const char*>(a.x) + r * a.ldx * ES;
-    char* const yr = static_cast<char*>(a.y) + r * a.ldy * ES;
-    float x[NV * VEC];
-    float s = 0.0f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const uint32_t c = (v * 64 * WPR + t) * VEC;
-      Vec<BF16, VEC> w;
-      if (c < C) w.load(xr, c);
-      else w.zero();
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) x[v * VEC + k] = w.get(k);
-    }
-#pragma unroll
-    for (int k = 0; k < NV * VEC; ++k) s = s + x[k];
-    const float mean = block_sum<WPR>(s, red) / (float)a.C;
-    float q = 0.0f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const bool live = (v * 64 * WPR + t) * VEC < C;
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        x[v * VEC + k] = live ? x[v * VEC + k] - mean : 0.0f;
-        q = __builtin_fmaf(x[v * VEC + k], x[v * VEC + k], q);
-      }
-    }
-    const float rstd = 1.0f / __builtin_sqrtf(block_sum<WPR>(q, red) / (float)a.C + a.eps);
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const uint32_t c = (v * 64 * WPR + t) * VEC;
-      if (c < C) {
-        float w[VEC], b[VEC], y[VEC];
-        load_param<VEC>(a.weight, a.w_bf16, c, 1.0f, w);
-        load_param<VEC>(a.bias, a.w_bf16, c, 0.0f, b);
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) y[k] = __builtin_fmaf(x[v * VEC + k] * rstd, w[k], b[k]);
-        Vec<BF16, VEC>::store(yr, c, y);
-      }
-    }
-    if (t == 0) {
-      if (a.mean) a.mean[r] = mean;
-      if (a.rstd) a.rstd[r] = rstd;
-    }
-  }
-}
-
-constexpr int BW = 8;                           // waves of a backward workgroup
+constexpr int BW = 8;                           // waves of a workgroup
 
 // Two sums over a row group of WPR waves; red[2] alternates between the rows
 // of a workgroup's walk, so one barrier per row is enough (a wave can write
@@ -314,6 +258,94 @@ __device__ __forceinline__ void group_sum2(float& p, float& q, float2 (*red)[BW]
   for (int i = 1; i < WPR; ++i) {
     p = p + red[turn][w0 + i].x;
     q = q + red[turn][w0 + i].y;
+  }
+}
+
+template <int WPR>
+__device__ __forceinline__ float group_sum(float p, float (*red)[BW], int turn) {
+  p = wave_sum(p);
+  if (WPR == 1) return p;
+  const int w = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) red[turn][w] = p;
+  __syncthreads();
+  const int w0 = w / WPR * WPR;
+  p = red[turn][w0];
+#pragma unroll
+  for (int i = 1; i < WPR; ++i) p = p + red[turn][w0 + i];
+  return p;
+}
+
+// Each wave holds its columns of weight and bias, and requests a row while the
+// row before it is worked on.
+template <bool BF16, int VEC, int NV, int WPR>
+__global__ __launch_bounds__(64 * BW) void k_norm(NormArgs a) {
+  constexpr int RPB = BW / WPR, RL = 64 * WPR;  // row groups, lanes per row
+  constexpr int ES = BF16 ? 2 : 4;
+  __shared__ float red[2][2][BW];               // mean and variance, each alternating
+  const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / RL);
+  const uint32_t t = threadIdx.x % RL, C = (uint32_t)a.C;
+  float w[NV * VEC], b[NV * VEC];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const uint32_t c = (v * RL + t) * VEC;
+    load_param<VEC>(c < C ? a.weight : nullptr, a.w_bf16, c, 1.0f, w + v * VEC);
+    load_param<VEC>(c < C ? a.bias : nullptr, a.w_bf16, c, 0.0f, b + v * VEC);
+  }
+  Vec<BF16, VEC> next[NV];
+  auto load = [&](int64_t r) {
+    const char* const xr = static_cast<const char*>(a.x) + (r < a.R ? r : 0) * a.ldx * ES;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const uint32_t c = (v * RL + t) * VEC;
+      if (r < a.R && c < C) next[v].load(xr, c);
+      else next[v].zero();
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t base = (int64_t)blockIdx.x * RPB;
+  load(base + sub);
+  // every wave of the workgroup makes the same number of passes (they share
+  // the barriers)
+  for (int turn = 0; base < a.R; base += step, turn ^= 1) {
+    const int64_t r = base + sub;
+    float x[NV * VEC], s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        x[v * VEC + k] = next[v].get(k);
+        s = s + x[v * VEC + k];
+      }
+    if (base + step < a.R) load(r + step);
+    const float mean = group_sum<WPR>(s, red[0], turn) / (float)a.C;
+    float q = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const bool live = (v * RL + t) * VEC < C;
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        x[v * VEC + k] = live ? x[v * VEC + k] - mean : 0.0f;
+        q = __builtin_fmaf(x[v * VEC + k], x[v * VEC + k], q);
+      }
+    }
+    const float rstd = 1.0f / __builtin_sqrtf(group_sum<WPR>(q, red[1], turn) / (float)a.C + a.eps);
+    if (r >= a.R) continue;
+    char* const yr = static_cast<char*>(a.y) + r * a.ldy * ES;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const uint32_t c = (v * RL + t) * VEC;
+      if (c < C) {
+        float y[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+          y[k] = __builtin_fmaf(x[v * VEC + k] * rstd, w[v * VEC + k], b[v * VEC + k]);
+        Vec<BF16, VEC>::store(yr, c, y);
+      }
+    }
+    if (t == 0) {
+      if (a.mean) a.mean[r] = mean;
+      if (a.rstd) a.rstd[r] = rstd;
+    }
   }
 }
 
@@ -471,6 +503,11 @@ __global__ __launch_bounds__(1024) void k_norm_dw_sum(const float* __restrict__ 
 
 // Partial rows of dw and db: workgroups of k_norm_backward (one per CU) and row
 // groups of k_norm_dw_any.
+// Workgroups of k_norm per CU: 16384 x 2880 bf16 41.6 us with 1, 37.7 with 2,
+// 41.2 with 3; single elements per lane need more waves (4099 x 1111 bf16 13.5
+// us with 2, 9.8 with 3, 9.2 with 4, 10.7 with 8).
+template <int VEC>
+constexpr int64_t norm_per_cu() { return VEC == 1 ? 4 : 2; }
 constexpr int64_t MOST_GROUPS = 256;
 int64_t norm_groups(int64_t R) { return R < MOST_GROUPS ? R : MOST_GROUPS; }
 
@@ -486,9 +523,10 @@ bool norm_vec(int64_t C, bool bf16, std::initializer_list<int64_t> ld, std::init
 
 template <bool BF16, int VEC, int NV, int WPR>
 int64_t start_norm(const NormArgs& a, hipStream_t st) {
-  constexpr int RPB = norm_threads<WPR>() / (64 * WPR);
-  hipLaunchKernelGGL((k_norm<BF16, VEC, NV, WPR>), dim3(row_grid((a.R + RPB - 1) / RPB)), dim3(norm_threads<WPR>()), 0,
-                     st, a);
+  constexpr int RPB = BW / WPR;
+  const int64_t want = (a.R + RPB - 1) / RPB, most = norm_per_cu<VEC>() * (int64_t)cu_count();
+  hipLaunchKernelGGL((k_norm<BF16, VEC, NV, WPR>), dim3((unsigned)(want < most ? want : most)), dim3(64 * BW), 0, st,
+                     a);
   return 1;
 }
 
@@ -509,19 +547,17 @@ int64_t start_norm_backward(const NormBwdArgs& a, hipStream_t st) {
 template <bool BF16, int VEC>
 int64_t try_norm(const NormArgs& a, hipStream_t st) {
   if constexpr (VEC == 8) {
-    MX_NV(start_norm, 1, 1) MX_NV(start_norm, 2, 1) MX_NV(start_norm, 3, 1) MX_NV(start_norm, 4, 1)
-    MX_NV(start_norm, 5, 1) MX_NV(start_norm, 6, 1)
-    MX_NV(start_norm, 2, 4) MX_NV(start_norm, 3, 4) MX_NV(start_norm, 4, 4) MX_NV(start_norm, 6, 4)
-    MX_NV(start_norm, 2, 16) MX_NV(start_norm, 4, 16)
+    MX_NV(start_norm, 1, 1) MX_NV(start_norm, 2, 1) MX_NV(start_norm, 3, 1) MX_NV(start_norm, 2, 2)
+    MX_NV(start_norm, 3, 2) MX_NV(start_norm, 2, 4) MX_NV(start_norm, 3, 4) MX_NV(start_norm, 2, 8)
+    MX_NV(start_norm, 3, 8) MX_NV(start_norm, 4, 8) MX_NV(start_norm, 5, 8)
   } else if constexpr (VEC == 4) {
     MX_NV(start_norm, 1, 1) MX_NV(start_norm, 2, 1) MX_NV(start_norm, 4, 1) MX_NV(start_norm, 6, 1)
-    MX_NV(start_norm, 8, 1) MX_NV(start_norm, 12, 1)
-    MX_NV(start_norm, 4, 4) MX_NV(start_norm, 6, 4) MX_NV(start_norm, 8, 4) MX_NV(start_norm, 12, 4)
-    MX_NV(start_norm, 4, 16) MX_NV(start_norm, 6, 16)
+    MX_NV(start_norm, 4, 2) MX_NV(start_norm, 6, 2) MX_NV(start_norm, 4, 4) MX_NV(start_norm, 6, 4)
+    MX_NV(start_norm, 4, 8) MX_NV(start_norm, 6, 8) MX_NV(start_norm, 8, 8)
   } else {
-    MX_NV(start_norm, 2, 1) MX_NV(start_norm, 4, 1) MX_NV(start_norm, 8, 1) MX_NV(start_norm, 12, 1)
-    MX_NV(start_norm, 18, 1) MX_NV(start_norm, 24, 1) MX_NV(start_norm, 8, 4) MX_NV(start_norm, 12, 4)
-    MX_NV(start_norm, 16, 4) MX_NV(start_norm, 24, 4) MX_NV(start_norm, 8, 16)
+    MX_NV(start_norm, 2, 1) MX_NV(start_norm, 4, 1) MX_NV(start_norm, 8, 1) MX_NV(start_norm, 6, 2)
+    MX_NV(start_norm, 9, 2) MX_NV(start_norm, 6, 4) MX_NV(start_norm, 9, 4) MX_NV(start_norm, 6, 8)
+    MX_NV(start_norm, 9, 8) MX_NV(start_norm, 12, 8) MX_NV(start_norm, 18, 8) MX_NV(start_norm, 24, 8)
   }
   return 0;
 }
@@ -540,8 +576,8 @@ int64_t try_norm_backward(const NormBwdArgs& a, hipStream_t st) {
     MX_NV(start_norm_backward, 6, 8)
   } else {
     MX_NV(start_norm_backward, 2, 1) MX_NV(start_norm_backward, 4, 1) MX_NV(start_norm_backward, 8, 1)
-    MX_NV(start_norm_backward, 12, 1) MX_NV(start_norm_backward, 18, 1) MX_NV(start_norm_backward, 12, 2)
-    MX_NV(start_norm_backward, 18, 2) MX_NV(start_norm_backward, 12, 4) MX_NV(start_norm_backward, 18, 4)
+    MX_NV(start_norm_backward, 12, 1) MX_NV(start_norm_backward, 9, 2) MX_NV(start_norm_backward, 12, 2)
+    MX_NV(start_norm_backward, 9, 4) MX_NV(start_norm_backward, 12, 4) MX_NV(start_norm_backward, 9, 8)
     MX_NV(start_norm_backward, 12, 8) MX_NV(start_norm_backward, 18, 8)
   }
   return 0;
