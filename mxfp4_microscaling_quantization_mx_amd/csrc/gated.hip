@@ -300,11 +300,14 @@ struct TileStage {
 template <int F>
 __device__ __forceinline__ void fetch_units(const TileLoad<F>& l, uint4 v[TileLoad<F>::N], int d, int kbytes, int tid) {
   using L = TileLoad<F>;
+  // (a stage past the row's end adds no scalar offset: the bounds check
+  // subtracts it from the buffer's size)
+  const uint32_t at = d * L::RB < kbytes ? (uint32_t)(d * L::RB) : 0u;
 #pragma unroll
   for (int i = 0; i < L::N; ++i) {
     const int left = kbytes - d * L::RB - 16 * ((tid + 256 * i) % L::U);
     const uint32_t off = left > 0 ? l.off[i] : PAST;
-    v[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(l.r, off, (uint32_t)(d * L::RB), 0));
+    v[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(l.r, off, at, 0));
     if (F > 2 && left < 16) v[i].z = v[i].w = 0u;
   }
 }

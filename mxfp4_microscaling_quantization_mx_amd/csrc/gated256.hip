@@ -61,8 +61,9 @@ bool gated256_layout_ok(const GatedArgs& a) {
   const bool words = a.A.ld_scales % 16 == 0 && a.B.ld_scales % 16 == 0 && a.stride_scales % 16 == 0 &&
                      (uintptr_t)a.A.scales % 16 == 0 && (uintptr_t)a.B.scales % 16 == 0;
   const int64_t arows = a.offsets ? 256 : a.M;
-  const bool small = arows * a.A.ld_codes < lim && 2 * a.N * a.B.ld_codes < lim && a.A.ld_scales < lim &&
-                     256 * a.ldo * 4 < lim && 256 * a.lddh * 4 < lim;
+  const bool small = arows * a.A.ld_codes < lim && 2 * a.N * a.B.ld_codes < lim && arows * a.A.ld_scales < lim &&
+                     2 * a.N * a.B.ld_scales < lim && 256 * a.ldo * 4 < lim && 256 * a.lddh * 4 < lim &&
+                     a.K < (1ll << 30);
   const int64_t slots = a.offsets ? (a.M + 255) / 256 + a.E : (a.M + 255) / 256;
   return a.a_elem == 0 && a.b_elem == 0 && words && small && (!a.offsets || a.E <= GG_EMAX) &&
          slots * ((a.N + 127) / 128) < lim;

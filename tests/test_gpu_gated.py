@@ -271,6 +271,48 @@ def test_grouped_offsets_are_clamped():
         check(H[lo:hi], ref, tol, False)
 
 
+def test_more_experts_than_the_pipelines_table():
+    """1000 experts, some empty, 8300 rows: past the tile pipelines' table."""
+    need_gpu()
+    rng = np.random.default_rng(21)
+    counts = rng.integers(0, 18, 1000)
+    counts[-1] += max(0, 8300 - counts.sum())
+    off, qa, a, qb, bs = _grouped(rng, counts, int(counts.sum()), 1000, 64, 64)
+    banner("grouped gated 1000 experts")
+    H = host(mx.grouped_gemm_gated(qa, to_dev(off), qb, CLAMPED, torch.float32))
+    for e in list(range(0, 1000, 37)) + [999]:
+        lo, hi = off[e], off[e + 1]
+        if hi > lo:
+            ref, tol = forward_ref(*projections(a[lo:hi], bs[e]), CLAMPED)
+            check(H[lo:hi], ref, tol, False, what=f"expert {e}")
+
+
+@pytest.mark.parametrize("M", [3, 200, 1100])
+def test_graph_replays_equal_eager_calls(M):
+    """A captured forward and backward pass, replayed between eager calls on
+    changing inputs."""
+    need_gpu()
+    rng = np.random.default_rng(31)
+    qb, _ = operand(rng, 2 * 272, 288, std=0.1)
+    inputs = [operand(rng, M, 288)[0] for _ in range(3)]
+    qa = operand(rng, M, 288)[0]
+    dh = torch.randn(M, 272, device="cuda")
+    run = lambda q: (mx.gemm_gated(q, qb, CLAMPED, torch.float32),
+                     mx.gemm_gated_backward(q, qb, dh, CLAMPED, torch.float32))
+    banner(f"gated graph M={M}")
+    run(qa)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run(qa)
+    for q in inputs:
+        qa.codes.copy_(q.codes)
+        qa.scales.copy_(q.scales)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, run(q)))
+
+
 @pytest.mark.parametrize("M,N", [(20, 24), (300, 160)])
 def test_nan_scales_poison_their_outputs_only(M, N):
     """A NaN scale of an A row makes that row NaN, one of a gate or up row its

@@ -228,3 +228,27 @@ def test_same_bits_every_run(R, C, dtype):
     ref, tol = backward(f64(dy), f64(x), f64(one[1]), f64(one[2]), np.ones(C))
     near(host(one[4]), ref[1], tol[1], "dweight")
     near(host(one[5]), ref[2], tol[2], "dbias")
+
+
+def test_graph_replays_equal_eager_calls():
+    """A captured forward and backward pass, replayed between eager calls."""
+    need_gpu()
+    x, dy = torch.randn(1000, 2880, device="cuda"), torch.randn(1000, 2880, device="cuda")
+    w, b = torch.randn(2880, device="cuda"), torch.randn(2880, device="cuda")
+
+    def run():
+        f = mx.layer_norm(x, w, b)
+        return f + mx.layer_norm_backward(dy, x, f[1], f[2], w) + (mx.dropout(x, 0.3, 5, 6, residual=dy),)
+
+    banner("norm and dropout graph")
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run()
+    for k in range(3):
+        x.normal_()
+        dy.normal_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, run())), k
