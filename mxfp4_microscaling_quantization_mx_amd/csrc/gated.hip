@@ -11,9 +11,9 @@
 //    split K 8 ways; the B tile is the 32 weight rows of the columns' gates
 //    (first 16) and ups (last 16).  For few rows, where reading the weight
 //    once with as many loads in flight as possible is all that counts.
-//  * k_gated_tile: 128 rows by 64 hidden columns per workgroup of 8 waves (2 x
-//    2 of 64 x 32, K split in two), operands staged through LDS; a wave's two B
-//    tiles are its columns' gates and ups.
+//  * k_gated_tile: 128 rows by 64 hidden columns per workgroup of 8 waves,
+//    operands staged through a ring in LDS; a wave's two B tiles are its
+//    columns' gates and ups.
 #include "gate_device.h"
 #include "mx_device.h"
 #include "mx_launch.h"
@@ -274,217 +274,260 @@ __device__ __forceinline__ void finish16(const GatedArgs& a, const GateP& p, int
   }
 }
 
-// Rows of one operand of k_gated_tile: 128 rows x 128 K-elements per stage, in
-// 16-byte units, staged through registers into LDS by the 256 threads of a K
-// half.  Every thread keeps its rows over all stages.
-template <int F>
-struct TileLoad {
-  static constexpr int RB = 16 * elem_bits<F>();      // code bytes of a stage row
-  static constexpr int U = RB / 16, N = 128 * U / 256;
-  static constexpr int PITCH = RB + 16;               // LDS row pitch: rows start in different banks
-  __amdgpu_buffer_rsrc_t r;                           // raw buffer: loads past its end return zeros
-  uint32_t off[N];                                    // this thread's units of stage 0
-};
-constexpr uint32_t PAST = 0xFFFFFF00u;                // an offset past any operand taken here
+// ---------------------------------------------------------------- 128 rows x 64 columns
+// A stage is 128 K-elements of the tile's 128 rows of A and 128 of B: LDS row
+// r of B is the gate (r % 64 < 32) or up row of hidden column n0 + 32 (r / 64)
+// + r % 32.  Codes and scale words go straight from global memory to LDS, into
+// one of RING slots, RING - 1 stages ahead of the one multiplied: with one
+// workgroup per CU nothing else hides the latency of the loads.  Waves 0-3
+// multiply the first 64 elements of every stage and waves 4-7 the rest, 2 x 2
+// waves of 64 rows by 32 columns each, and add their sums at the end: 64 KiB of
+// LDS reads per stage in MXFP8, where 8 waves of 32 x 32 read 96 (21.9 us
+// against 22.7).  One barrier per stage.  LDS rows hold the stage's codes in
+// 16-byte chunks, XOR-swizzled so that 16 consecutive rows reading one chunk
+// hit different banks.
+//
+// 512 x 2880 x 2880: MXFP4 17.8 us, MXFP8 23.4, of which 7.5 are the launch, the
+// first loads and the epilogue, and the rest 0.41 and 0.67 us per stage: 10 and
+// 12 TB/s out of the XCDs' L2s, which a larger tile would lower and leave CUs
+// idle for.  Staged through registers with two LDS buffers: 18.9 and 28.2.
+// RING 3 or 5 (with a remainder to take per stage) costs MXFP4 1 us, MXFP8
+// none; 8 slots MXFP4 1 us.
+typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+constexpr uint32_t PAST = 0x80000000u;           // a buffer offset past any operand (taken below 2 GiB)
 
-// One stage of both operands in registers: codes, and the four scale bytes of
-// one row (threads 0 .. 127 A rows, 128 .. 255 B rows).
+template <int F>
+struct TileOp {
+  static constexpr int RB = 16 * elem_bits<F>(); // code bytes of a stage row (64, 96 or 128)
+  static constexpr int PITCH = F == 0 ? 64 : 128;
+  static constexpr int CH = PITCH / 16;          // chunks of an LDS row
+  static constexpr int LOADS = 128 * CH / 512;   // 1 KiB loads per wave and stage
+  static constexpr int BYTES = 128 * PITCH;
+  static __device__ __forceinline__ int key(int row) { return F == 0 ? (row >> 2) & 3 : (row >> 1) & 7; }
+};
+
 template <int FA, int FB>
-struct TileStage {
-  uint4 a[TileLoad<FA>::N], b[TileLoad<FB>::N];
-  uint32_t sc;
+struct TileSlot {
+  static constexpr int SCALES = TileOp<FA>::BYTES + TileOp<FB>::BYTES;   // per wave 64 words, the first 32 rows'
+  static constexpr int BYTES = SCALES + 2048;
+  static constexpr int RING = 4;                 // (a power of two: the slot of a stage is a mask)
+  static constexpr int LOADS = TileOp<FA>::LOADS + TileOp<FB>::LOADS + 1;
 };
 
-// Units of stage d (K-elements 128 d ..); units past the row's end read zeros,
-// and of a unit that an FP6 row ends inside only the first half is kept.
-template <int F>
-__device__ __forceinline__ void fetch_units(const TileLoad<F>& l, uint4 v[TileLoad<F>::N], int d, int kbytes, int tid) {
-  using L = TileLoad<F>;
-  // (a stage past the row's end adds no scalar offset: the bounds check
-  // subtracts it from the buffer's size)
-  const uint32_t at = d * L::RB < kbytes ? (uint32_t)(d * L::RB) : 0u;
-#pragma unroll
-  for (int i = 0; i < L::N; ++i) {
-    const int left = kbytes - d * L::RB - 16 * ((tid + 256 * i) % L::U);
-    const uint32_t off = left > 0 ? l.off[i] : PAST;
-    v[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(l.r, off, at, 0));
-    if (F > 2 && left < 16) v[i].z = v[i].w = 0u;
-  }
+// One load of a wave straight into LDS: 16 or 4 bytes per lane, at dst + 16 or
+// 4 times the lane.
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t off, uint32_t so) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)dst, 16, off, so, 0, 0);
+}
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t off, uint32_t so) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)dst, 4, off, so, 0, 0);
 }
 
+// LDS row of lane `lane` of load i of wave `wave`.
 template <int F>
-__device__ __forceinline__ void put_units(const uint4 v[TileLoad<F>::N], uint8_t* lds, int tid) {
-  using L = TileLoad<F>;
-#pragma unroll
-  for (int i = 0; i < L::N; ++i) {
-    const int id = tid + 256 * i, r = id / L::U, u = id % L::U;
-    *reinterpret_cast<uint4*>(lds + r * L::PITCH + 16 * u) = v[i];
-  }
+__device__ __forceinline__ int tile_row(int wave, int lane, int i) {
+  return (64 / TileOp<F>::CH) * (wave * TileOp<F>::LOADS + i) + lane / TileOp<F>::CH;
 }
 
-// This lane's operand registers of 64-deep step s from its LDS row.
+// One operand's loads of this wave: per load the row's offset and its chunk.
 template <int F>
-__device__ __forceinline__ v8i read_units(const uint8_t* row, int s, int hi) {
+struct TileLoads {
+  using O = TileOp<F>;
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t row[O::LOADS];
+  int chunk[O::LOADS];
+
+  // Request stage d into LDS at dst.  Chunks past the stage row or the row's
+  // end read zeros; a stage past the row's end adds no scalar offset (the
+  // bounds check subtracts it from the buffer's size).
+  __device__ __forceinline__ void issue(int d, int kbytes, uint8_t* dst, int wave) const {
+    const int at = d * O::RB;
+    const uint32_t so = at < kbytes ? (uint32_t)at : 0u;
+#pragma unroll
+    for (int i = 0; i < O::LOADS; ++i) {
+      const int c16 = 16 * chunk[i];
+      const bool live = c16 < O::RB && at + c16 < kbytes;
+      load_lds16(r, dst + 1024 * (wave * O::LOADS + i), live ? row[i] + c16 : PAST, so);
+    }
+  }
+};
+
+// The operand registers of 64-deep step `step` for this lane's rows of two row
+// tiles (LDS addresses `row` and 32 rows on) and their scale words (LDS
+// addresses sc and 64 words on), in one asm block that waits for itself only
+// (the compiler would wait for every load in flight).
+template <int F>
+__device__ __forceinline__ void tile_read(uint32_t row, int key, int hi, int step, uint32_t sc, v8i out[2],
+                                          uint32_t sw[2]) {
   if constexpr (elem_bits<F>() == 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(row + 32 * s + 16 * hi);
-    return v8i{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+    v4i x, y;
+    asm volatile(
+        "ds_read_b32 %2, %5\n\tds_read_b32 %3, %5 offset:256\n\t"
+        "ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:2048\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(x), "=&v"(y), "=&v"(sw[0]), "=&v"(sw[1])
+        : "v"(row + 16 * ((2 * step + hi) ^ key)), "v"(sc)
+        : "memory");
+    out[0] = v8i{x[0], x[1], x[2], x[3], 0, 0, 0, 0};
+    out[1] = v8i{y[0], y[1], y[2], y[3], 0, 0, 0, 0};
   } else if constexpr (elem_bits<F>() == 8) {
-    const uint4 x = *reinterpret_cast<const uint4*>(row + 64 * s + 16 * hi);
-    const uint4 y = *reinterpret_cast<const uint4*>(row + 64 * s + 32 + 16 * hi);
-    return v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
+    v4i x[4];
+    asm volatile(
+        "ds_read_b32 %4, %8\n\tds_read_b32 %5, %8 offset:256\n\t"
+        "ds_read_b128 %0, %6\n\tds_read_b128 %1, %7\n\t"
+        "ds_read_b128 %2, %6 offset:4096\n\tds_read_b128 %3, %7 offset:4096\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(sw[0]), "=&v"(sw[1])
+        : "v"(row + 16 * ((4 * step + hi) ^ key)), "v"(row + 16 * ((4 * step + 2 + hi) ^ key)), "v"(sc)
+        : "memory");
+#pragma unroll
+    for (int t = 0; t < 2; ++t) out[t] = __builtin_shufflevector(x[2 * t], x[2 * t + 1], 0, 1, 2, 3, 4, 5, 6, 7);
   } else {
-    const uint2* q = reinterpret_cast<const uint2*>(row + 48 * s + 24 * hi);
-    const uint2 x = q[0], y = q[1], z = q[2];
-    return v8i{(int)x.x, (int)x.y, (int)y.x, (int)y.y, (int)z.x, (int)z.y, 0, 0};
+    // the lane's 24-byte block, as 8-byte reads inside chunks
+    uint32_t at[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int o = 48 * step + 24 * hi + 8 * k;
+      at[k] = row + 16 * ((o >> 4) ^ key) + (o & 15);
+    }
+    v2i x[6];
+    asm volatile(
+        "ds_read_b32 %6, %11\n\tds_read_b32 %7, %11 offset:256\n\t"
+        "ds_read_b64 %0, %8\n\tds_read_b64 %1, %9\n\tds_read_b64 %2, %10\n\tds_read_b64 %3, %8 offset:4096\n\t"
+        "ds_read_b64 %4, %9 offset:4096\n\tds_read_b64 %5, %10 offset:4096\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]), "=&v"(sw[0]), "=&v"(sw[1])
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(sc)
+        : "memory");
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      out[t] = v8i{x[3 * t][0], x[3 * t][1], x[3 * t + 1][0], x[3 * t + 1][1], x[3 * t + 2][0], x[3 * t + 2][1], 0, 0};
   }
 }
 
-// 128 rows by 64 hidden columns.  Waves 0-3 take the first half of the K
-// stages and waves 4-7 the second, 2 x 2 waves of 64 rows by 32 columns each;
-// LDS row r of B is the gate (r % 64 < 32) or up row of hidden column
-// n0 + 32 (r / 64) + r % 32.  Each half has two LDS buffers and holds one more
-// stage in registers, or two where both operands are small (HELD): stage s + 1
-// is written to LDS and stage s + 1 + HELD requested while stage s is
-// multiplied, since with few workgroups the kernel is bound by the latency of
-// its loads.
 template <int FA, int FB>
 __global__ __launch_bounds__(512) void k_gated_tile(GatedArgs a, GateP p, int64_t tiles, int64_t tiles_n, int a_words,
                                                     int b_words) {
-  using LA = TileLoad<FA>;
-  using LB = TileLoad<FB>;
-  constexpr int ABYTES = 128 * LA::PITCH, BBYTES = 128 * LB::PITCH, BUF = ABYTES + BBYTES + 1024;
-  constexpr int RED = 8 * 2 * 16 * 64 * 4;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[4 * BUF > RED ? 4 * BUF : RED];
+  using OA = TileOp<FA>;
+  using OB = TileOp<FB>;
+  using SL = TileSlot<FA, FB>;
+  static_assert(SL::RING * SL::BYTES >= 8 * 2 * 16 * 64 * 4, "the K halves are added through the ring's LDS");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[SL::RING * SL::BYTES];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wk = wave >> 2, wm = (wave >> 1) & 1, wn = wave & 1, l32 = lane & 31, hi = lane >> 5;
+  const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)lds;
+  const int nkb = (int)(a.K / 32), stages = (nkb + 3) / 4;
+  const int abytes = (int)(a.K * elem_bits<FA>() / 8), bbytes = (int)(a.K * elem_bits<FB>() / 8);
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int64_t slot = t / tiles_n;
-    const int64_t n0 = (t - slot * tiles_n) * 64;
+    const int n0 = (int)(t - slot * tiles_n) * 64;
     if (n0 >= a.N) continue;                          // (columns are padded to 8 tiles)
     int ex, rows;
     int64_t row0;
     if (!place_slot<128>(a, slot, ex, row0, rows)) return;  // past the last tile
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wk = w >> 2, wm = (w >> 1) & 1, wn = w & 1, tid = threadIdx.x & 255;
-    const int l32 = lane & 31, hi = lane >> 5;
-    MxOperand B = a.B;
-    B.codes += ex * a.stride_codes;
-    B.scales += ex * a.stride_scales;
+    const uint8_t* const bc = a.B.codes + ex * a.stride_codes;
+    const uint8_t* const bs = a.B.scales + ex * a.stride_scales;
     // rows and columns past the end read the last one; their results are dropped
-    auto a_row = [&](int r) { return row0 + (r < rows ? r : rows - 1); };
+    auto a_row = [&](int r) { return r < rows ? r : rows - 1; };
     auto b_row = [&](int r) {
-      const int64_t c = n0 + 32 * (r >> 6) + (r & 31), n = c < a.N ? c : a.N - 1;
-      const int up = (r >> 5) & 1;
-      return a.halves ? up * a.N + n : 2 * n + up;
+      const int c = n0 + 32 * (r >> 6) + (r & 31), n = c < a.N ? c : (int)a.N - 1, up = (r >> 5) & 1;
+      return a.halves ? up * (int)a.N + n : 2 * n + up;
     };
-    LA la;
-    LB lb;
+    TileLoads<FA> la;
+    TileLoads<FB> lb;
     la.r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.A.codes + row0 * a.A.ld_codes), 0,
                                              (uint32_t)(rows * a.A.ld_codes), 0x00020000);
-    lb.r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(B.codes), 0, (uint32_t)(2 * a.N * B.ld_codes),
+    lb.r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(bc), 0, (uint32_t)(2 * a.N * a.B.ld_codes),
                                              0x00020000);
 #pragma unroll
-    for (int i = 0; i < LA::N; ++i) {
-      const int id = tid + 256 * i;
-      la.off[i] = (uint32_t)((a_row(id / LA::U) - row0) * a.A.ld_codes) + 16u * (id % LA::U);
+    for (int i = 0; i < OA::LOADS; ++i) {
+      const int r = tile_row<FA>(wave, lane, i);
+      la.row[i] = (uint32_t)(a_row(r) * (int)a.A.ld_codes);
+      la.chunk[i] = (lane % OA::CH) ^ OA::key(r);
     }
 #pragma unroll
-    for (int i = 0; i < LB::N; ++i) {
-      const int id = tid + 256 * i;
-      lb.off[i] = (uint32_t)(b_row(id / LB::U) * B.ld_codes) + 16u * (id % LB::U);
+    for (int i = 0; i < OB::LOADS; ++i) {
+      const int r = tile_row<FB>(wave, lane, i);
+      lb.row[i] = (uint32_t)(b_row(r) * (int)a.B.ld_codes);
+      lb.chunk[i] = (lane % OB::CH) ^ OB::key(r);
     }
-    const bool sa = tid < 128;                        // wave-uniform
-    const int64_t sr = sa ? a_row(tid) : b_row(tid - 128);
-    const uint8_t* sp = sa ? a.A.scales + (a.a_2d ? sr >> 5 : sr) * a.A.ld_scales
-                           : B.scales + (a.b_2d ? sr >> 5 : sr) * B.ld_scales;
-    const bool words = sa ? a_words : b_words;
-    const int nkb = (int)(a.K / 32), stages = (nkb + 3) / 4, per = (stages + 1) / 2;
-    const int abytes = (int)(a.K * elem_bits<FA>() / 8), bbytes = (int)(a.K * elem_bits<FB>() / 8);
-    const int d0 = wk * per;                          // stages past the last are zeros at scale 1
-    auto fetch = [&](TileStage<FA, FB>& st, int s) {
-      const int d = d0 + s;
-      fetch_units<FA>(la, st.a, d, abytes, tid);
-      fetch_units<FB>(lb, st.b, d, bbytes, tid);
-      if (words && 4 * d + 4 <= nkb) {
-        st.sc = *reinterpret_cast<const uint32_t*>(sp + 4 * (int64_t)d);
-      } else {
+    // scale words: waves 0-3 32 rows of A each, 4-7 of B, in the lower half-wave
+    const bool sa = wave < 4;
+    const int sr = sa ? a_row(32 * wave + l32) : b_row(32 * (wave - 4) + l32);
+    const int64_t s0 = sa ? row0 : 0;                 // (A's rows count from row0)
+    const bool s2 = sa ? a.a_2d : a.b_2d;
+    const int64_t sld = sa ? a.A.ld_scales : a.B.ld_scales;
+    const int64_t sfirst = s2 ? s0 >> 5 : s0, slast = s2 ? (s0 + (sa ? rows : 2 * a.N) - 1) >> 5
+                                                         : s0 + (sa ? rows : 2 * a.N) - 1;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>((sa ? a.A.scales : bs) + sfirst * sld), 0, (uint32_t)((slast - sfirst + 1) * sld),
+        0x00020000);
+    const int64_t srow = s2 ? ((s0 + sr) >> 5) - sfirst : sr;
+    const uint32_t soff = hi ? PAST : (uint32_t)(srow * sld);
+    auto issue = [&](int d) {
+      uint8_t* const q = lds + (d % SL::RING) * SL::BYTES;
+      la.issue(d, abytes, q, wave);
+      lb.issue(d, bbytes, q + OA::BYTES, wave);
+      const bool in = d < stages;
+      if (sa ? a_words : b_words) {
+        load_lds4(rs, q + SL::SCALES + 256 * wave, in ? soff : PAST, in ? 4u * d : 0u);
+      } else {                        // rows that do not start at a word: bytes, waiting for every load
         uint32_t v = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v |= (4 * d + j < nkb ? (uint32_t)sp[4 * (int64_t)d + j] : 127u) << (8 * j);
-        st.sc = v;
+        for (int j = 0; j < 4; ++j)
+          v |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rs, 4 * d + j < nkb ? soff + 4 * d + j : PAST, 0, 0)
+               << (8 * j);
+        *reinterpret_cast<uint32_t*>(q + SL::SCALES + 256 * wave + 4 * lane) = v;
       }
-    };
-    uint8_t* const mine = smem + 2 * BUF * wk;
-    auto put = [&](const TileStage<FA, FB>& st, int buf) {
-      uint8_t* const q = mine + buf * BUF;
-      put_units<FA>(st.a, q, tid);
-      put_units<FB>(st.b, q + ABYTES, tid);
-      reinterpret_cast<uint32_t*>(q + ABYTES + BBYTES)[tid] = st.sc;
     };
     v16f acc[2][2];
     acc[0][0] = acc[0][1] = acc[1][0] = acc[1][1] = zero16();
-    auto multiply = [&](int buf) {
-      const uint8_t* const q = mine + buf * BUF;
-      const uint32_t* const sw = reinterpret_cast<const uint32_t*>(q + ABYTES + BBYTES);
-      int xa[2], xb[2];
+    if (stages > 0)
+#pragma unroll 1
+      for (int d = 0; d < SL::RING - 1; ++d) issue(d);
+    for (int s = 0; s < stages; ++s) {
+      // this wave's loads of stage s landed (and its own writes to LDS; those of
+      // the RING - 2 stages after it may be on their way), then every wave's; and
+      // every wave is done with stage s - 1, whose slot takes stage s + RING - 1
+      constexpr int N = (SL::RING - 2) * SL::LOADS;
+      static_assert(N <= 63, "the counter has 6 bits");
+      __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4));
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      issue(s + SL::RING - 1);
+      const uint32_t q = base + (uint32_t)((s % SL::RING) * SL::BYTES);
+      const int ra = 64 * wm + l32, rb = 64 * wn + l32;
+      uint32_t xa[2], xb[2];
+      v8i va[2], vb[2];
+      tile_read<FA>(q + ra * OA::PITCH, OA::key(ra), hi, wk, q + SL::SCALES + 512 * wm + 4 * l32, va, xa);
+      tile_read<FB>(q + OA::BYTES + rb * OB::PITCH, OB::key(rb), hi, wk, q + SL::SCALES + 1024 + 512 * wn + 4 * l32, vb,
+                    xb);
+      // scale bytes of blocks past K become 0, a finite scale: their codes are
+      // zero, or 8 bytes of an FP6 row's padding that vanish at 2^-127 squared
+      const int kb = 2 * wk + hi;
+      const uint32_t keep = 4 * s + kb < nkb ? 0xFFu : 0u;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        xa[i] = (int)(sw[64 * wm + 32 * i + l32] >> (8 * hi));
-        xb[i] = (int)(sw[128 + 64 * wn + 32 * i + l32] >> (8 * hi));
-      }
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        v8i va[2], vb[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          va[i] = read_units<FA>(q + (64 * wm + 32 * i + l32) * LA::PITCH, s, hi);
-          vb[i] = read_units<FB>(q + ABYTES + (64 * wn + 32 * i + l32) * LB::PITCH, s, hi);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (s == 0)
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(va[i], vb[j], acc[i][j], mfma_fmt<FA>(),
-                                                                           mfma_fmt<FB>(), 0, xa[i], 0, xb[j]);
-            else
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(va[i], vb[j], acc[i][j], mfma_fmt<FA>(),
-                                                                           mfma_fmt<FB>(), 2, xa[i], 2, xb[j]);
-          }
-      }
-    };
-    constexpr int HELD = elem_bits<FA>() + elem_bits<FB>() <= 10 ? 2 : 1;
-    TileStage<FA, FB> st[HELD];
-    if (per > 0) {
-      fetch(st[0], 0);
-      if (HELD > 1 && per > 1) fetch(st[HELD - 1], 1);
-      put(st[0], 0);
-      if (per > HELD) fetch(st[0], HELD);
-      __syncthreads();
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              va[i], vb[j], acc[i][j], mfma_fmt<FA>(), mfma_fmt<FB>(), 0, (int)((xa[i] >> (8 * kb)) & keep), 0,
+              (int)((xb[j] >> (8 * kb)) & keep));
     }
-    // stage s + 1 is in st[(s + 1) % HELD]; buffer (s + 1) % 2 was last read in
-    // stage s - 1, before the last barrier
-    for (int s = 0; s < per; s += 2) {
-      if (s + 1 < per) put(st[1 % HELD], 1);
-      if (s + 1 + HELD < per) fetch(st[1 % HELD], s + 1 + HELD);
-      multiply(0);
-      __syncthreads();
-      if (s + 1 >= per) break;
-      if (s + 2 < per) put(st[0], 0);
-      if (s + 2 + HELD < per) fetch(st[0], s + 2 + HELD);
-      multiply(1);
-      __syncthreads();
-    }
+    __builtin_amdgcn_s_waitcnt(0x0070);               // the loads past the last stage write zeros
+    __syncthreads();
     // the two K halves: wave wk finishes row tile wk and hands over the other
-    float (*red)[2][16][64] = reinterpret_cast<float (*)[2][16][64]>(smem);
+    float (*red)[2][16][64] = reinterpret_cast<float (*)[2][16][64]>(lds);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) red[w][j][r][lane] = wk ? acc[0][j][r] : acc[1][j][r];
+      for (int r = 0; r < 16; ++r) red[wave][j][r][lane] = wk ? acc[0][j][r] : acc[1][j][r];
     __syncthreads();
     v16f gu[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) gu[j][r] = (wk ? acc[1][j][r] : acc[0][j][r]) + red[w ^ 4][j][r][lane];
+      for (int r = 0; r < 16; ++r) gu[j][r] = (wk ? acc[1][j][r] : acc[0][j][r]) + red[wave ^ 4][j][r][lane];
     const int sub = 64 * wm + 32 * wk;
     const uint32_t col = (uint32_t)n0 + 32 * wn + l32;
     if (p.act == 0) finish16<0>(a, p, row0, sub, rows, col, hi, gu[0], gu[1]);
@@ -517,8 +560,9 @@ hipError_t launch_direct(const GatedArgs& a, bool few, hipStream_t st) {
   const int a_words = a.A.ld_scales % 4 == 0 && (uintptr_t)a.A.scales % 4 == 0;
   const int b_words = a.B.ld_scales % 4 == 0 && (uintptr_t)a.B.scales % 4 == 0 && a.stride_scales % 4 == 0;
   // k_gated_tile addresses its rows and the weight operand with 32-bit offsets
-  const int64_t lim = 0xFFFFFF00ll;
-  const bool fits = 128 * a.A.ld_codes < lim && 2 * a.N * a.B.ld_codes < lim && 128 * a.ldo + 2 * a.N < lim / 4 &&
+  const int64_t lim = 1ll << 31;
+  const bool fits = 128 * a.A.ld_codes < lim && 2 * a.N * a.B.ld_codes < lim &&
+                    128 * a.A.ld_scales < lim && 2 * a.N * a.B.ld_scales < lim && 128 * a.ldo + 2 * a.N < lim / 4 &&
                     128 * a.lddh < lim / 4;
   if (few || !fits) {
     const int64_t tiles_n = column_tiles(a, 16), tiles = tiles_n * slot_bound(a, 32);
@@ -545,24 +589,28 @@ hipError_t launch_direct_b(const GatedArgs& a, bool few, hipStream_t st) {
 
 }  // namespace
 
-// Which kernel (N = K = 2880 unless said; MXFP4, then MXFP8):
-//  * k_gated_few while its workgroups are at most 3 per CU: 128 rows 13-16 us
-//    against k_gated_tile's 16 (23 / 26), 192 rows 21 / 17 (38 / 26), 1024 rows
-//    of 512 x 1024 8.8 / 9.7 (16 / 13).  Grouped, whose weights are read from
-//    HBM, up to 8 rows per expert (32 experts, 64 rows 53 us against the
+// Which kernel (us, N = K = 2880 unless said; MXFP4, then MXFP8):
+//  * k_gated_few while its workgroups are at most 3 per CU in MXFP4, 2.5 with
+//    wider elements: 128 rows 15.8 against k_gated_tile's 16.2 (23.7 / 21.8),
+//    192 rows 21 / 16.5 (38 / 22), 256 rows of 1440 x 2912 16.1 / 16.1 (24.1 /
+//    21.7), 192 rows 13.4 / 16.0 (20.3 / 21.4).  Grouped, whose weights are read
+//    from HBM, up to 8 rows per expert (32 experts, 64 rows 53 against the
 //    pipeline's 68, 256 rows 79 / 78, 512 rows 104 / 83; MXFP8 100 / 140, 137 /
-//    147) or 6 workgroups per CU (512 x 1024: 512 rows 11 / 15 us, 1024 rows
-//    15 / 15).
-//  * k_gated_tile while one workgroup per CU does: 16-18 us (24-28) against the
-//    21-24 (44-48) of a pipeline that is not full; with two per CU 33-37
-//    (53-57).  Also everything that the pipelines do not take.
-//  * the 256-row pipelines beyond.
+//    147) or 6 workgroups per CU (512 x 1024: 512 rows 11 / 15, 1024 rows 15 /
+//    15).
+//  * k_gated_tile while one workgroup per CU does in MXFP4, 16-18 against the
+//    21-24 of a pipeline that is not full and 32 with two; while two do with
+//    wider elements, 22-24 with one, 43 with two against the pipeline's 47-49
+//    (MXFP6 41-43 / 40-45).  Also everything that the pipelines do not take.
+//  * the 256-row pipelines beyond, and for groups (2048 rows over 32 experts 89
+//    against k_gated_tile's 125; MXFP8 169 / 182).
 hipError_t launch_gated(const GatedArgs& a, hipStream_t st) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
   const int64_t cus = cu_count();
   const int64_t few_wgs = (a.N + 15) / 16 * slot_bound(a, 32), tile_wgs = (a.N + 63) / 64 * slot_bound(a, 128);
-  const bool few = a.offsets ? a.M <= 8 * (int64_t)a.E || few_wgs <= 6 * cus : few_wgs <= 3 * cus;
-  if (!few && (a.offsets || tile_wgs > cus)) {
+  const bool f4 = a.a_elem == 0 && a.b_elem == 0;
+  const bool few = a.offsets ? a.M <= 8 * (int64_t)a.E || few_wgs <= 6 * cus : 2 * few_wgs <= (f4 ? 6 : 5) * cus;
+  if (!few && (a.offsets || tile_wgs > (f4 ? 1 : 2) * cus)) {
     if (gated256_layout_ok(a)) return launch_gated256(a, st);
     if (gated_f8_layout_ok(a)) return launch_gated_f8(a, st);
   }
