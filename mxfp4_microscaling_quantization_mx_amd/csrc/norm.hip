@@ -22,8 +22,8 @@
 //    doubled partial rows), each lane also keeping its sums of dw and db; the
 //    workgroup's row groups are added through LDS at the end and stored as one
 //    partial row [2][C].  16384 x 2880 bf16: 51 us, 5.6 TB/s (72 us with one
-//    wave per row, the weights read again and no row ahead); 4099 x 1111
-//    float32, unaligned: 16 us, 3.5 TB/s.
+//    wave per row, the weights read again and no row ahead), 57 with the sum of
+//    the partial rows; 4099 x 1111 float32, unaligned: 16 us, 3.5 TB/s.
 //  * k_norm_any, k_norm_dx_any, k_norm_dw_any: rows too long for registers,
 //    read once per sum (the later reads come from cache), the weight's
 //    gradient by columns.
