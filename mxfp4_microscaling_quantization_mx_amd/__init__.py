@@ -136,11 +136,12 @@ def _check(status):
 def _stream(t):
     # the handle of torch.cuda.current_stream(t.device), without building the
     # Stream object (2 us of a 4 us launch)
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(t.get_device()))
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+    # an int (None: a null pointer), which the declared argument types convert
+    return t.data_ptr() if t is not None else None
 
 
 @dataclass
