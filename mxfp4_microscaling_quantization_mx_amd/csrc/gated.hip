@@ -7,8 +7,8 @@
 // (launch_gated).  They run on V_MFMA_SCALE_F32_32X32X64_F8F6F4, 128 K-elements
 // of a row at a time; waves that split the K range add their partial tiles
 // through LDS in a fixed order.
-//  * k_gated_few: 32 rows by 16 hidden columns per workgroup of 8 waves, which
-//    split K 8 ways; the B tile is the 32 weight rows of the columns' gates
+//  * k_gated_few: 32 rows by 16 hidden columns per workgroup of 8 or 2 waves,
+//    which split K; the B tile is the 32 weight rows of the columns' gates
 //    (first 16) and ups (last 16).  For few rows, where reading the weight
 //    once with as many loads in flight as possible is all that counts.
 //  * k_gated_tile: 128 rows by 64 hidden columns per workgroup of 8 waves,
@@ -188,18 +188,22 @@ __device__ __forceinline__ void finish(const GatedArgs& a, const GateP& p, int64
 }
 
 // k_gated_few reads every weight byte once per 32 rows straight into MFMA
-// operand registers, one wave an eighth of K, so that 2880 columns are 180
-// workgroups of 8 waves with loads in flight on every CU.  One row of N = K =
-// 2880 in MXFP4 takes 4.6 us on the GPU (8.8 MB of weights that earlier runs
-// left in the caches) and 8.0 with the call; 64 rows over 32 experts, 22 of them
-// with rows, 53-60 us: 3.3 TB/s of weights.
-constexpr int FW = 8;               // waves of k_gated_few, splitting K
+// operand registers; its FW waves split K.  8 waves up to 2.5 workgroups per CU,
+// so that 2880 columns are 180 workgroups with loads in flight on every CU; 2
+// beyond, where a wave's longer walk along K has its loads in flight for more
+// of a workgroup's life and 20 waves fit a CU (16 as two workgroups of 8).  us
+// with 8, 4, 2 and 1 waves: 128 x 2880 x 2880 MXFP4 15.6, 13.1, 13.6, 16.1 (90
+// rows 12.5, 12.9, 13.2, 15.3); 64 rows over 32 experts, 22 of them with rows,
+// 53, 48, 43, 45 (MXFP8 100, 96, 95, 104), and 52-56 with the weights out of
+// the caches (59-62 with 8): 3.6 TB/s.  One row of N = K = 2880 takes 4.6 us on
+// the GPU (8.8 MB of weights that earlier runs left in the caches) and 7.8 with
+// the call.
 // Pieces a wave requests before it multiplies the first.  More would cost the
 // second workgroup per CU its registers: 64 rows over 32 MXFP8 experts 100 us
 // with 2, 145 with 3; MXFP4 53 with 2 or 3, 85 with 4.
 constexpr int FD = 2;
 
-template <int FA, int FB>
+template <int FA, int FB, int FW>
 __global__ __launch_bounds__(64 * FW) void k_gated_few(GatedArgs a, GateP p, int64_t tiles, int64_t tiles_n,
                                                        int a_words, int b_words) {
   __shared__ float red[FW][32][33];
@@ -238,8 +242,11 @@ __global__ __launch_bounds__(64 * FW) void k_gated_few(GatedArgs a, GateP p, int
 #pragma unroll
     for (int r = 0; r < 16; ++r) red[w][8 * (r >> 2) + 4 * hi + (r & 3)][l32] = acc[r];
     __syncthreads();
-    const int row = threadIdx.x >> 4, col = threadIdx.x & 15;
-    if (row < rows && n0 + col < a.N) {
+    const int col = threadIdx.x & 15;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 4 * FW) {
+      const int row = r0 + (threadIdx.x >> 4);
+      if (row >= rows || n0 + col >= a.N) break;
       float g = red[0][row][col], u = red[0][row][col + 16];
 #pragma unroll
       for (int i = 1; i < FW; ++i) {
@@ -572,8 +579,12 @@ hipError_t launch_direct(const GatedArgs& a, bool few, hipStream_t st) {
                     128 * a.lddh < lim / 4;
   if (few || !fits) {
     const int64_t tiles_n = column_tiles(a, 16), tiles = tiles_n * slot_bound(a, 32);
-    hipLaunchKernelGGL((k_gated_few<FA, FB>), dim3(tile_grid(tiles)), dim3(64 * FW), 0, st, a, p, tiles, tiles_n,
-                       a_words, b_words);
+    if (2 * tiles <= 5 * (int64_t)cu_count())
+      hipLaunchKernelGGL((k_gated_few<FA, FB, 8>), dim3(tile_grid(tiles)), dim3(512), 0, st, a, p, tiles, tiles_n,
+                         a_words, b_words);
+    else
+      hipLaunchKernelGGL((k_gated_few<FA, FB, 2>), dim3(tile_grid(tiles)), dim3(128), 0, st, a, p, tiles, tiles_n,
+                         a_words, b_words);
   } else {
     const int64_t tiles_n = column_tiles(a, 64), tiles = tiles_n * slot_bound(a, 128);
     hipLaunchKernelGGL((k_gated_tile<FA, FB>), dim3(tile_grid(tiles)), dim3(512), 0, st, a, p, tiles, tiles_n, a_words,
@@ -597,12 +608,12 @@ hipError_t launch_direct_b(const GatedArgs& a, bool few, hipStream_t st) {
 
 // Which kernel (us, N = K = 2880 unless said; MXFP4, then MXFP8):
 //  * k_gated_few while its workgroups are at most 3 per CU in MXFP4, 2.5 with
-//    wider elements: 128 rows 15.8 against k_gated_tile's 16.2 (23.7 / 21.8),
+//    wider elements: 128 rows 13.6 against k_gated_tile's 16.2 (23.7 / 21.8),
 //    192 rows 21 / 16.5 (38 / 22), 256 rows of 1440 x 2912 16.1 / 16.1 (24.1 /
 //    21.7), 192 rows 13.4 / 16.0 (20.3 / 21.4).  Grouped, whose weights are read
-//    from HBM, up to 8 rows per expert (32 experts, 64 rows 53 against the
-//    pipeline's 68, 256 rows 79 / 78, 512 rows 104 / 83; MXFP8 100 / 140, 137 /
-//    147) or 6 workgroups per CU (512 x 1024: 512 rows 11 / 15, 1024 rows 15 /
+//    from HBM, up to 8 rows per expert (32 experts, 64 rows 43 against the
+//    pipeline's 68, 256 rows 70 / 78, 512 rows about 90 / 83; MXFP8 95 / 140, 136
+//    / 147) or 6 workgroups per CU (512 x 1024: 512 rows 11 / 15, 1024 rows 15 /
 //    15).
 //  * k_gated_tile while one workgroup per CU does in MXFP4, 16-18 against the
 //    21-24 of a pipeline that is not full and 32 with two; while two do with

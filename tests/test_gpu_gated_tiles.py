@@ -75,7 +75,16 @@ def test_pipelines(ea, eb, M, N, K, layout):
     run_case(M, N, K, mx.Gate("silu", 1.702, 1.25, 1.0, layout), ea, eb, out=torch.bfloat16, dh_dtype=torch.bfloat16)
 
 
-@pytest.mark.parametrize("counts,N,K", [([700, 0, 3, 256, 257, 0], 720, 288), ([1025, 1, 0, 511], 640, 96)])
+@pytest.mark.parametrize("ea,eb", [("e2m1", "e2m1"), ("e4m3", "e5m2"), ("e2m3", "e3m2"), ("e3m2", "e2m1")])
+@pytest.mark.parametrize("M,N,K", [(97, 2880, 96), (33, 6000, 32), (128, 2890, 544), (100, 2881, 2880)])
+def test_few_rows_of_many_columns(ea, eb, M, N, K):
+    """More than 2.5 workgroups per CU of the kernel for few rows: K split over
+    2 waves, with none, one or several pieces each."""
+    need_gpu()
+    run_case(M, N, K, TIGHT, ea, eb)
+
+
+@pytest.mark.parametrize("counts,N,K", [([1] * 39 + [33], 720, 288), ([700, 0, 3, 256, 257, 0], 720, 288), ([1025, 1, 0, 511], 640, 96)])
 @pytest.mark.parametrize("ea,eb", [("e2m1", "e2m1"), ("e4m3", "e4m3"), ("e2m3", "e5m2"), ("e4m3", "e2m1")])
 @pytest.mark.parametrize("layout", ["interleaved", "halves"])
 def test_grouped_tiles(counts, N, K, ea, eb, layout):
