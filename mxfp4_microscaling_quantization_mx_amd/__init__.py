@@ -133,10 +133,25 @@ def _check(status):
         raise MXError(status, _lib.mx_last_error().decode())
 
 
-def _stream(t):
+def _stream(t, *others):
+    """The current stream of t's device, once every tensor of the call (None:
+    not given) is known to be there: the library sees addresses only, and a
+    host address would fault the GPU."""
     # the handle of torch.cuda.current_stream(t.device), without building the
-    # Stream object (2 us of a 4 us launch)
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    # Stream object (2 us of a 4 us launch); a host tensor's index is -1, which
+    # would pass for the current device
+    d = t.get_device()
+    if d < 0:
+        raise ValueError("operands must be CUDA tensors")
+    for o in others:
+        if o is not None and o.get_device() != d:
+            raise ValueError("operands must be CUDA tensors on one device")
+    return torch._C._cuda_getCurrentRawStream(d)
+
+
+def _parts(q):
+    """The tensors of an MX operand that may be absent."""
+    return (q.codes, q.scales) if q is not None else ()
 
 
 def _ptr(t):
@@ -200,6 +215,7 @@ def quantize(x, axis="last", block="1d", rounding="rne", rht_mask=None, seed=0, 
         raise ValueError("quantize expects a 2-D bf16/float32 CUDA tensor")
     if x.stride(1) != 1:
         raise ValueError("quantize expects a row-major tensor (stride(1) == 1)")
+    st = _stream(x, *_parts(out))
     R, C = x.shape
     rows, K = (C, R) if axis == "dim0" else (R, C)
     if out is None:
@@ -209,7 +225,7 @@ def quantize(x, axis="last", block="1d", rounding="rne", rht_mask=None, seed=0, 
                     offset & (2**64 - 1))
     ot = out.c_struct()
     _check(lib.mx_quantize(_ptr(x), _DTYPE[x.dtype], R, C, x.stride(0), ctypes.byref(cfg),
-                           ctypes.byref(ot), _stream(x)))
+                           ctypes.byref(ot), st))
     return out
 
 
@@ -223,6 +239,7 @@ def clip_count(x, axis="last", block="1d", rht_mask=None, scale_mode="floor", el
         raise ValueError("clip_count expects a 2-D bf16/float32 CUDA tensor")
     if x.stride(1) != 1:
         raise ValueError("clip_count expects a row-major tensor (stride(1) == 1)")
+    st = _stream(x, out)
     if out is None:
         out = torch.zeros(1, dtype=torch.int64, device=x.device)
     elif out.dtype != torch.int64 or out.numel() != 1 or not out.is_cuda:
@@ -231,7 +248,7 @@ def clip_count(x, axis="last", block="1d", rht_mask=None, scale_mode="floor", el
     cfg = QuantCfgC(_AXIS[axis], _BLOCK[block], _ROUND["rne"], int(rht_mask is not None),
                     (rht_mask or 0) & 0xFFFFFFFF, _SCALE[scale_mode], 0, 0)
     _check(lib.mx_clip_count(_ptr(x), _DTYPE[x.dtype], R, C, x.stride(0), ctypes.byref(cfg), _ELEM[elem][0],
-                             _ptr(out), _stream(x)))
+                             _ptr(out), st))
     return out
 
 
@@ -246,6 +263,7 @@ def quantize_gather(x, rows, rounding="rne", rht_mask=None, seed=0, offset=0, ou
         raise ValueError("quantize_gather expects a row-major tensor (stride(1) == 1)")
     if rows.dtype != torch.int32 or rows.dim() != 1 or not rows.is_cuda or not rows.is_contiguous():
         raise ValueError("quantize_gather expects rows as a contiguous 1-D int32 CUDA tensor")
+    st = _stream(x, rows, *_parts(out))
     R, C = x.shape
     n = rows.shape[0]
     if out is None:
@@ -255,7 +273,7 @@ def quantize_gather(x, rows, rounding="rne", rht_mask=None, seed=0, offset=0, ou
                     offset & (2**64 - 1))
     ot = out.c_struct()
     _check(lib.mx_quantize_gather(_ptr(x), _DTYPE[x.dtype], R, C, x.stride(0), _ptr(rows), n,
-                                  ctypes.byref(cfg), ctypes.byref(ot), _stream(x)))
+                                  ctypes.byref(cfg), ctypes.byref(ot), st))
     return out
 
 
@@ -269,6 +287,7 @@ def quantize_scatter(x, dest, k, rows_out=None, rht_mask=None, out=None, scale_m
         raise ValueError("quantize_scatter expects a 2-D bf16/float32 CUDA tensor")
     if x.stride(1) != 1:
         raise ValueError("quantize_scatter expects a row-major tensor (stride(1) == 1)")
+    st = _stream(x, dest, *_parts(out))
     R, C = x.shape
     if dest.dtype != torch.int32 or not dest.is_cuda or not dest.is_contiguous() or dest.numel() != R * k:
         raise ValueError("quantize_scatter expects dest as a contiguous int32 CUDA tensor of R*k entries")
@@ -278,19 +297,20 @@ def quantize_scatter(x, dest, k, rows_out=None, rht_mask=None, out=None, scale_m
                     (rht_mask or 0) & 0xFFFFFFFF, _SCALE[scale_mode], 0, 0)
     ot = out.c_struct()
     _check(lib.mx_quantize_scatter(_ptr(x), _DTYPE[x.dtype], R, C, x.stride(0), _ptr(dest), k,
-                                   ctypes.byref(cfg), ctypes.byref(ot), _stream(x)))
+                                   ctypes.byref(cfg), ctypes.byref(ot), st))
     return out
 
 
 def dequantize(q, dtype=torch.float32, inverse_rht_mask=None, out=None):
     """Decode an MX operand to a [rows, K] tensor (see mx_dequantize)."""
     lib = load_library()
+    st = _stream(q.codes, q.scales, out)
     if out is None:
         out = torch.empty((q.rows, q.K), dtype=dtype, device=q.codes.device)
     qt = q.c_struct()
     _check(lib.mx_dequantize(ctypes.byref(qt), int(inverse_rht_mask is not None),
                              (inverse_rht_mask or 0) & 0xFFFFFFFF, _ptr(out), _DTYPE[out.dtype],
-                             out.stride(0), _stream(out)))
+                             out.stride(0), st))
     return out
 
 
@@ -298,10 +318,11 @@ def transpose(q, out=None):
     """Exact transpose of an operand with 2-D (32x32) blocks: [R, C] -> [C, R]
     (see mx_transpose)."""
     lib = load_library()
+    st = _stream(q.codes, q.scales, *_parts(out))
     if out is None:
         out = empty_mx(q.K, q.rows, "2d", device=q.codes.device, elem=q.elem)
     it, ot = q.c_struct(), out.c_struct()
-    _check(lib.mx_transpose(ctypes.byref(it), ctypes.byref(ot), _stream(q.codes)))
+    _check(lib.mx_transpose(ctypes.byref(it), ctypes.byref(ot), st))
     return out
 
 
@@ -314,9 +335,11 @@ def gemm_workspace(M, N, K, device="cuda"):
     leaves it fit for the next, see mx_gemm_workspace_size).  Calls that share
     it must not overlap, so callers on several streams pass their own."""
     n = load_library().mx_gemm_workspace_size(M, N, K)
+    dev = torch.device(device)
+    if dev.type != "cuda":
+        raise ValueError("gemm_workspace: the workspace is a CUDA tensor")
     if not n:
         return None
-    dev = torch.device(device)
     key = dev.index if dev.index is not None else torch.cuda.current_device()
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < n:
@@ -331,6 +354,7 @@ def gemm(a, b, out_dtype=torch.float32, out=None, workspace=None):
     tensor of at least mx_gemm_workspace_size bytes) or the per-device one of
     gemm_workspace."""
     lib = load_library()
+    st = _stream(a.codes, a.scales, b.codes, b.scales, out, workspace)
     if out is None:
         out = torch.empty((a.rows, b.rows), dtype=out_dtype, device=a.codes.device)
     ws = lib.mx_gemm_workspace_size(a.rows, b.rows, a.K)
@@ -339,7 +363,7 @@ def gemm(a, b, out_dtype=torch.float32, out=None, workspace=None):
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     at, bt = a.c_struct(), b.c_struct()
     _check(lib.mx_gemm(ctypes.byref(at), ctypes.byref(bt), _ptr(out), _DTYPE[out.dtype],
-                       out.stride(0), _ptr(workspace), nbytes, _stream(out)))
+                       out.stride(0), _ptr(workspace), nbytes, st))
     return out
 
 
@@ -348,11 +372,12 @@ def gemm_noalloc(a, b, out_dtype=torch.float32, out=None):
     no workspace argument (for callers that cannot allocate; the output is
     still the caller's)."""
     lib = load_library()
+    st = _stream(a.codes, a.scales, b.codes, b.scales, out)
     if out is None:
         out = torch.empty((a.rows, b.rows), dtype=out_dtype, device=a.codes.device)
     at, bt = a.c_struct(), b.c_struct()
     _check(lib.mx_gemm_noalloc(ctypes.byref(at), ctypes.byref(bt), _ptr(out), _DTYPE[out.dtype], out.stride(0),
-                               _stream(out)))
+                               st))
     return out
 
 
@@ -363,6 +388,7 @@ def gemm_fused_quant_a(a, b, out_dtype=torch.float32, out=None, rht_mask=None, s
     lib = load_library()
     if a.dim() != 2 or a.dtype not in _DTYPE or not a.is_cuda or a.stride(1) != 1:
         raise ValueError("gemm_fused_quant_a expects a row-major 2-D bf16 CUDA tensor")
+    st = _stream(a, b.codes, b.scales, out)
     M, K = a.shape
     if out is None:
         out = torch.empty((M, b.rows), dtype=out_dtype, device=a.device)
@@ -370,7 +396,7 @@ def gemm_fused_quant_a(a, b, out_dtype=torch.float32, out=None, rht_mask=None, s
                     (rht_mask or 0) & 0xFFFFFFFF, _SCALE[scale_mode], 0, 0)
     bt = b.c_struct()
     _check(lib.mx_gemm_fused_quant_a(_ptr(a), _DTYPE[a.dtype], M, K, a.stride(0), ctypes.byref(cfg), ctypes.byref(bt),
-                                     _ptr(out), _DTYPE[out.dtype], out.stride(0), _stream(out)))
+                                     _ptr(out), _DTYPE[out.dtype], out.stride(0), st))
     return out
 
 
@@ -378,11 +404,12 @@ def gemm_quantize(a, b, scale_mode="floor", out=None):
     """A * B^T quantized along N into an MXFP4 operand [M, N] (1-D blocks, RNE)
     in the GEMM epilogue (see mx_gemm_quantize)."""
     lib = load_library()
+    st = _stream(a.codes, a.scales, b.codes, b.scales, *_parts(out))
     if out is None:
         out = empty_mx(a.rows, b.rows, device=a.codes.device)
     at, bt, ot = a.c_struct(), b.c_struct(), out.c_struct()
     _check(lib.mx_gemm_quantize(ctypes.byref(at), ctypes.byref(bt), _SCALE[scale_mode], ctypes.byref(ot),
-                                _stream(out.codes)))
+                                st))
     return out
 
 
@@ -396,6 +423,7 @@ def grouped_gemm(a, offsets, b, out_dtype=torch.bfloat16, out=None):
     E = b.codes.shape[0]
     if offsets.dtype != torch.int32 or not offsets.is_cuda or offsets.numel() != E + 1:
         raise ValueError("offsets must be an int32 CUDA tensor with E+1 entries")
+    st = _stream(a.codes, a.scales, b.codes, b.scales, offsets, out)
     N = b.codes.shape[1]
     if out is None:
         out = torch.empty((a.rows, N), dtype=out_dtype, device=a.codes.device)
@@ -404,7 +432,7 @@ def grouped_gemm(a, offsets, b, out_dtype=torch.bfloat16, out=None):
     at = a.c_struct()
     _check(lib.mx_grouped_gemm(ctypes.byref(at), _ptr(offsets), E, ctypes.byref(b0),
                                b.codes.stride(0), b.scales.stride(0), _ptr(out),
-                               _DTYPE[out.dtype], out.stride(0), _stream(out)))
+                               _DTYPE[out.dtype], out.stride(0), st))
     return out
 
 
@@ -416,6 +444,7 @@ def grouped_gemm_quantize(a, offsets, b, scale_mode="floor", out=None):
     E = b.codes.shape[0]
     if offsets.dtype != torch.int32 or not offsets.is_cuda or offsets.numel() != E + 1:
         raise ValueError("offsets must be an int32 CUDA tensor with E+1 entries")
+    st = _stream(a.codes, a.scales, b.codes, b.scales, offsets, *_parts(out))
     N = b.codes.shape[1]
     if out is None:
         out = empty_mx(a.rows, N, device=a.codes.device)
@@ -424,7 +453,7 @@ def grouped_gemm_quantize(a, offsets, b, scale_mode="floor", out=None):
     at, ot = a.c_struct(), out.c_struct()
     _check(lib.mx_grouped_gemm_quantize(ctypes.byref(at), _ptr(offsets), E, ctypes.byref(b0), b.codes.stride(0),
                                         b.scales.stride(0), _SCALE[scale_mode], ctypes.byref(ot),
-                                        _stream(out.codes)))
+                                        st))
     return out
 
 
@@ -459,6 +488,7 @@ def _check_rows(t, what, shape=None, dtype=None):
 
 def _gated(what, a, b, gate, out, out_dtype, dh, offsets):
     lib = load_library()
+    st = _stream(a.codes, a.scales, b.codes, b.scales, offsets, dh, out)
     backward = dh is not None
     if offsets is not None:
         E, rows = b.codes.shape[0], b.codes.shape[1]
@@ -482,7 +512,7 @@ def _gated(what, a, b, gate, out, out_dtype, dh, offsets):
         args = (_ptr(dh), _DTYPE[dh.dtype], dh.stride(0))
     at, gc = a.c_struct(), gate.c_struct()
     _check(getattr(lib, what)(ctypes.byref(at), *group, ctypes.byref(gc), *args, _ptr(out), _DTYPE[out.dtype],
-                              out.stride(0), _stream(out)))
+                              out.stride(0), st))
     return out
 
 
@@ -525,6 +555,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None):
     layer_norm_backward."""
     lib = load_library()
     _check_rows(x, "layer_norm: x")
+    st = _stream(x, weight, bias, out)
     R, C = x.shape
     if weight is not None:
         _norm_param(weight, C, None, "layer_norm: weight")
@@ -538,7 +569,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None):
     wd = weight if weight is not None else bias
     _check(lib.mx_layer_norm(_ptr(x), _DTYPE[x.dtype], R, C, x.stride(0), _ptr(weight), _ptr(bias),
                              MX_DT_F32 if wd is None else _DTYPE[wd.dtype], eps, _ptr(out), out.stride(0),
-                             _ptr(mean), _ptr(rstd), _stream(x)))
+                             _ptr(mean), _ptr(rstd), st))
     return out, mean, rstd
 
 
@@ -549,6 +580,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, param_dtype=No
     lib = load_library()
     _check_rows(x, "layer_norm_backward: x")
     _check_rows(dy, "layer_norm_backward: dy", x.shape, x.dtype)
+    st = _stream(x, dy, mean, rstd, weight, out)
     R, C = x.shape
     for t, n in ((mean, "mean"), (rstd, "rstd")):
         if t.shape != (R,) or t.dtype != torch.float32 or not t.is_cuda or (R > 1 and t.stride(0) != 1):
@@ -567,7 +599,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, param_dtype=No
     ws = x.new_empty(nbytes, dtype=torch.uint8)
     _check(lib.mx_layer_norm_backward(_ptr(dy), _ptr(x), _DTYPE[x.dtype], R, C, dy.stride(0), x.stride(0), _ptr(mean),
                                       _ptr(rstd), _ptr(weight), _DTYPE[param_dtype], _ptr(out), out.stride(0),
-                                      _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes, _stream(x)))
+                                      _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes, st))
     return out, dweight, dbias
 
 
@@ -577,6 +609,7 @@ def dropout(x, p, seed=0, offset=0, residual=None, out=None):
     gradient with the same p, seed and offset and no residual."""
     lib = load_library()
     _check_rows(x, "dropout: x")
+    st = _stream(x, residual, out)
     R, C = x.shape
     ldr = 0
     if residual is not None:
@@ -587,7 +620,7 @@ def dropout(x, p, seed=0, offset=0, residual=None, out=None):
     else:
         _check_rows(out, "dropout: out", x.shape, x.dtype)
     _check(lib.mx_dropout(_ptr(x), _DTYPE[x.dtype], R, C, x.stride(0), p, seed & (2**64 - 1), offset & (2**64 - 1),
-                          _ptr(residual), ldr, _ptr(out), out.stride(0), _stream(x)))
+                          _ptr(residual), ldr, _ptr(out), out.stride(0), st))
     return out
 
 
