@@ -413,6 +413,12 @@ def gemm_quantize(a, b, scale_mode="floor", out=None):
     return out
 
 
+def _check_offsets(offsets, E):
+    if (offsets.dtype != torch.int32 or not offsets.is_cuda or offsets.numel() != E + 1
+            or not offsets.is_contiguous()):
+        raise ValueError("offsets must be a contiguous int32 CUDA tensor of E+1 entries")
+
+
 def grouped_gemm(a, offsets, b, out_dtype=torch.bfloat16, out=None):
     """MoE grouped GEMM (see mx_grouped_gemm).
 
@@ -421,8 +427,7 @@ def grouped_gemm(a, offsets, b, out_dtype=torch.bfloat16, out=None):
     (2-D) or [E, N, K/32] (1-D)."""
     lib = load_library()
     E = b.codes.shape[0]
-    if offsets.dtype != torch.int32 or not offsets.is_cuda or offsets.numel() != E + 1:
-        raise ValueError("offsets must be an int32 CUDA tensor with E+1 entries")
+    _check_offsets(offsets, E)
     st = _stream(a.codes, a.scales, b.codes, b.scales, offsets, out)
     N = b.codes.shape[1]
     if out is None:
@@ -442,8 +447,7 @@ def grouped_gemm_quantize(a, offsets, b, scale_mode="floor", out=None):
     grouped_gemm."""
     lib = load_library()
     E = b.codes.shape[0]
-    if offsets.dtype != torch.int32 or not offsets.is_cuda or offsets.numel() != E + 1:
-        raise ValueError("offsets must be an int32 CUDA tensor with E+1 entries")
+    _check_offsets(offsets, E)
     st = _stream(a.codes, a.scales, b.codes, b.scales, offsets, *_parts(out))
     N = b.codes.shape[1]
     if out is None:
@@ -492,8 +496,7 @@ def _gated(what, a, b, gate, out, out_dtype, dh, offsets):
     backward = dh is not None
     if offsets is not None:
         E, rows = b.codes.shape[0], b.codes.shape[1]
-        if offsets.dtype != torch.int32 or not offsets.is_cuda or offsets.numel() != E + 1:
-            raise ValueError("offsets must be an int32 CUDA tensor with E+1 entries")
+        _check_offsets(offsets, E)
         bt = MxTensorC(b.codes.data_ptr(), b.scales.data_ptr(), rows, b.K, b.codes.stride(1), b.scales.stride(1),
                        _BLOCK[b.block], _ELEM[b.elem][0])
         group = (_ptr(offsets), E, ctypes.byref(bt), b.codes.stride(0), b.scales.stride(0))

@@ -132,3 +132,20 @@ def test_stub_is_reached_when_nothing_is_wrong():
                                out=at(f32(4, 32), 0))
     with pytest.raises(Reached):
         mx.gemm(mxt(32, 0), mxt(48, 0), out=at(f32(32, 48), 0), workspace=at(torch.zeros(256, dtype=torch.uint8), 0))
+
+
+@pytest.mark.parametrize("offsets", [
+    torch.zeros(6, dtype=torch.int32)[::2], torch.zeros(1, dtype=torch.int32).expand(3),
+    torch.zeros(3, dtype=torch.int64), torch.zeros(4, dtype=torch.int32)])
+@pytest.mark.parametrize("name", ["grouped_gemm", "grouped_gemm_quantize", "grouped_gemm_gated",
+                                  "grouped_gemm_gated_backward"])
+def test_offsets_that_are_not_a_plain_int32_list_are_refused(name, offsets):
+    """The library reads E+1 consecutive integers: strided or expanded offsets
+    would be other numbers, or reach past their buffer."""
+    out = {"grouped_gemm": (32, 64), "grouped_gemm_gated": (32, 32), "grouped_gemm_gated_backward": (32, 64)}
+    kw = dict(out=at(f32(*out[name]), 0)) if name in out else dict(out=mxt(32, 0))
+    args = (mxt(32, 0), at(offsets, 0), mxt(64, 0, experts=2))
+    if name.endswith("backward"):
+        args += (at(f32(32, 32), 0),)
+    with pytest.raises(ValueError, match="offsets"):
+        getattr(mx, name)(*args, **kw)
