@@ -549,14 +549,16 @@ mx_status mx_grouped_gemm_gated_backward(const mx_tensor* A, const int32_t* d_gr
 /*
  * mx_layer_norm — y = (x - mean) * rstd * weight + bias over each row of x
  * [R, C], mean = sum x / C, rstd = 1 / sqrt(sum (x - mean)^2 / C + eps).  The
- * statistics and the formula are float32 (the variance from the centred
- * values, not from a difference of sums); y is rounded once.
+ * mean is summed in float64 and subtracted with what float32 leaves of it (a
+ * row of one value gives y = bias, whatever the value); the variance, from the
+ * centred values, and the formula are float32; y is rounded once.
  *
  *   x, y    device; [R, C] of `dtype` (mx_dtype, one type for both), row strides
  *           ldx, ldy elements (>= C); element-aligned.  y may be x itself.
  *   weight  device; [C] of w_dtype; NULL = 1.  bias: likewise; NULL = 0.
  *   eps     >= 0, finite.
- *   mean, rstd  device; float32 [R] each, for the backward pass; NULL = not stored.
+ *   mean, rstd  device; float32 [R] each, for the backward pass; NULL = not stored
+ *           (the mean rounded to float32).
  *   R or C = 0: nothing is written.  NaN or Inf in a row makes that row NaN.
  */
 mx_status mx_layer_norm(const void* x, int32_t dtype, int64_t R, int64_t C, int64_t ldx, const void* weight,

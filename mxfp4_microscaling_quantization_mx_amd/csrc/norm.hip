@@ -5,8 +5,10 @@
 //   dx = rstd * (gy - sum(gy) / C - xh * sum(gy xh) / C),  gy = dy * w
 //   dw = sum over rows of dy * xh,  db = sum over rows of dy
 //
-// Statistics and formulas are float32; the variance is taken from the centred
-// values (a difference of sums would cancel where |mean| >> the spread).
+// Statistics and formulas are float32, but for a row's mean, which is summed in
+// double and subtracted in two float32 parts (Mean); the variance is taken from
+// the centred values (a difference of sums would cancel where |mean| >> the
+// spread).
 //
 // Both directions are bound by HBM bandwidth (bf16: 4 bytes per element
 // forward, 6 backward; a device copy reaches 5.1 TB/s), so a row is read once
@@ -15,9 +17,9 @@
 //    VEC consecutive ones (16 bytes where the rows allow it, else single
 //    elements) of every NV-th piece of the row.  Workgroups of 8 waves walk
 //    the rows; each lane keeps its weights in registers and requests a row
-//    while the one before is worked on.  16384 x 2880 bf16: 34-38 us, 5.0-5.6
-//    TB/s (44 us with one row per wave, whose weights came through L2 each
-//    time).
+//    while the one before is worked on.  16384 x 2880 bf16: 38 us, 5.0 TB/s
+//    (44 us with one row per wave, whose weights came through L2 each time);
+//    the double sum is hidden behind the loads (37.7 with a float32 one).
 //  * k_norm_backward: the same, one workgroup per CU (two lost 10 % to the
 //    doubled partial rows), each lane also keeping its sums of dw and db; the
 //    workgroup's row groups are added through LDS at the end and stored as one
@@ -54,9 +56,12 @@ __device__ __forceinline__ float ldw(const void* p, bool bf16, int64_t i) {
 
 // Sum of v over the 64 lanes, in every lane: neighbours and quads by DPP, the
 // 16-lane rows by mirrors, then the gfx950 row and half-wave swaps.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#define MX_DPP_ADD(CTRL) \
-  v = v + __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true))
+#define MX_DPP_ADD(CTRL) v = v + __uint_as_float(dpp<CTRL>(__float_as_uint(v)))
   MX_DPP_ADD(0xB1);    // lane ^ 1
   MX_DPP_ADD(0x4E);    // lane ^ 2
   MX_DPP_ADD(0x141);   // the other quad of 8 lanes (half-row mirror)
@@ -69,19 +74,55 @@ __device__ __forceinline__ float wave_sum(float v) {
   const auto b = __builtin_amdgcn_permlane32_swap(t, t, false, false);
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
+__device__ __forceinline__ double from_words(uint32_t lo, uint32_t hi) {
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+#define MX_WORDS(V) const uint64_t q = __builtin_bit_cast(uint64_t, V); const uint32_t lo = (uint32_t)q, hi = (uint32_t)(q >> 32)
+#define MX_DPP_ADD(CTRL) { MX_WORDS(v); v = v + from_words(dpp<CTRL>(lo), dpp<CTRL>(hi)); }
+  MX_DPP_ADD(0xB1) MX_DPP_ADD(0x4E) MX_DPP_ADD(0x141) MX_DPP_ADD(0x140)
+#undef MX_DPP_ADD
+  {
+    MX_WORDS(v);
+    const auto a = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+    v = from_words(a[0], b[0]) + from_words(a[1], b[1]);
+  }
+  MX_WORDS(v);
+#undef MX_WORDS
+  const auto a = __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+  return from_words(a[0], b[0]) + from_words(a[1], b[1]);
+}
 
 // Sum of v over the WAVES waves of the workgroup, in every thread.
-template <int WAVES>
-__device__ __forceinline__ float block_sum(float v, float* red) {
+template <int WAVES, class T>
+__device__ __forceinline__ T block_sum(T v, T* red) {
   v = wave_sum(v);
   if (WAVES == 1) return v;
   __syncthreads();                              // red may still be read by the previous sum
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
-  float s = red[0];
+  T s = red[0];
 #pragma unroll
   for (int i = 1; i < WAVES; ++i) s = s + red[i];
   return s;
+}
+
+// A row's mean from its sum, as a float32 and what that leaves: subtracting both
+// keeps a centred value's error at its own roundings, where a float32 mean's 2^-24
+// |mean| would be in every value of the row and stay (a row of one value must
+// centre to zero).  The quotient is corrected to the last bit, so such a row's
+// mean is its value.
+struct Mean {
+  float hi, lo;
+  __device__ __forceinline__ float centre(float x) const { return (x - hi) - lo; }
+};
+__device__ __forceinline__ Mean row_mean(double sum, double C, double inv) {
+  double m = sum * inv;
+  m = __builtin_fma(__builtin_fma(-m, C, sum), inv, m);
+  const float hi = (float)m;
+  return {hi, (float)(m - (double)hi)};
 }
 
 constexpr int LW = 4;                           // waves per row of the any-width kernels
@@ -91,28 +132,30 @@ unsigned row_grid(int64_t R) { return (unsigned)(R < (1 << 20) ? R : (1 << 20));
 
 template <bool BF16>
 __global__ __launch_bounds__(64 * LW) void k_norm_any(NormArgs a) {
+  __shared__ double redm[LW];
   __shared__ float red[LW];
+  const double inv = 1.0 / (double)a.C;
   for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
     const char* x = static_cast<const char*>(a.x) + r * a.ldx * (BF16 ? 2 : 4);
     char* y = static_cast<char*>(a.y) + r * a.ldy * (BF16 ? 2 : 4);
-    float s = 0.0f;
-    for (int64_t c = threadIdx.x; c < a.C; c += 64 * LW) s = s + ld1<BF16>(x, c);
-    const float mean = block_sum<LW>(s, red) / (float)a.C;
+    double s = 0.0;
+    for (int64_t c = threadIdx.x; c < a.C; c += 64 * LW) s = s + (double)ld1<BF16>(x, c);
+    const Mean mean = row_mean(block_sum<LW>(s, redm), (double)a.C, inv);
     float q = 0.0f;
     for (int64_t c = threadIdx.x; c < a.C; c += 64 * LW) {
-      const float d = ld1<BF16>(x, c) - mean;
+      const float d = mean.centre(ld1<BF16>(x, c));
       q = __builtin_fmaf(d, d, q);
     }
     const float rstd = 1.0f / __builtin_sqrtf(block_sum<LW>(q, red) / (float)a.C + a.eps);
     // (y may be x: every element is read and written by the same thread)
     for (int64_t c = threadIdx.x; c < a.C; c += 64 * LW) {
-      const float xh = (ld1<BF16>(x, c) - mean) * rstd;
+      const float xh = mean.centre(ld1<BF16>(x, c)) * rstd;
       const float w = a.weight ? ldw(a.weight, a.w_bf16, c) : 1.0f;
       const float b = a.bias ? ldw(a.bias, a.w_bf16, c) : 0.0f;
       st1<BF16>(y, c, __builtin_fmaf(xh, w, b));
     }
     if (threadIdx.x == 0) {
-      if (a.mean) a.mean[r] = mean;
+      if (a.mean) a.mean[r] = mean.hi;
       if (a.rstd) a.rstd[r] = rstd;
     }
   }
@@ -261,8 +304,8 @@ __device__ __forceinline__ void group_sum2(float& p, float& q, float2 (*red)[BW]
   }
 }
 
-template <int WPR>
-__device__ __forceinline__ float group_sum(float p, float (*red)[BW], int turn) {
+template <int WPR, class T>
+__device__ __forceinline__ T group_sum(T p, T (*red)[BW], int turn) {
   p = wave_sum(p);
   if (WPR == 1) return p;
   const int w = threadIdx.x >> 6;
@@ -281,9 +324,11 @@ template <bool BF16, int VEC, int NV, int WPR>
 __global__ __launch_bounds__(64 * BW) void k_norm(NormArgs a) {
   constexpr int RPB = BW / WPR, RL = 64 * WPR;  // row groups, lanes per row
   constexpr int ES = BF16 ? 2 : 4;
-  __shared__ float red[2][2][BW];               // mean and variance, each alternating
+  __shared__ double redm[2][BW];                // mean and variance, each alternating
+  __shared__ float redv[2][BW];
   const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / RL);
   const uint32_t t = threadIdx.x % RL, C = (uint32_t)a.C;
+  const double inv = 1.0 / (double)a.C;
   float w[NV * VEC], b[NV * VEC];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
@@ -308,27 +353,28 @@ __global__ __launch_bounds__(64 * BW) void k_norm(NormArgs a) {
   // the barriers)
   for (int turn = 0; base < a.R; base += step, turn ^= 1) {
     const int64_t r = base + sub;
-    float x[NV * VEC], s = 0.0f;
+    float x[NV * VEC];
+    double s = 0.0;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
         x[v * VEC + k] = next[v].get(k);
-        s = s + x[v * VEC + k];
+        s = s + (double)x[v * VEC + k];
       }
     if (base + step < a.R) load(r + step);
-    const float mean = group_sum<WPR>(s, red[0], turn) / (float)a.C;
+    const Mean mean = row_mean(group_sum<WPR>(s, redm, turn), (double)a.C, inv);
     float q = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const bool live = (v * RL + t) * VEC < C;
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
-        x[v * VEC + k] = live ? x[v * VEC + k] - mean : 0.0f;
+        x[v * VEC + k] = live ? mean.centre(x[v * VEC + k]) : 0.0f;
         q = __builtin_fmaf(x[v * VEC + k], x[v * VEC + k], q);
       }
     }
-    const float rstd = 1.0f / __builtin_sqrtf(group_sum<WPR>(q, red[1], turn) / (float)a.C + a.eps);
+    const float rstd = 1.0f / __builtin_sqrtf(group_sum<WPR>(q, redv, turn) / (float)a.C + a.eps);
     if (r >= a.R) continue;
     char* const yr = static_cast<char*>(a.y) + r * a.ldy * ES;
 #pragma unroll
@@ -343,7 +389,7 @@ __global__ __launch_bounds__(64 * BW) void k_norm(NormArgs a) {
       }
     }
     if (t == 0) {
-      if (a.mean) a.mean[r] = mean;
+      if (a.mean) a.mean[r] = mean.hi;
       if (a.rstd) a.rstd[r] = rstd;
     }
   }
