@@ -451,17 +451,20 @@ __global__ __launch_bounds__(64 * BW) void k_norm_backward(NormBwdArgs a) {
     if (base + step < a.R) load(next, r + step);
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v) {
+      // a row and a column past the end have dy = 0 and xh = 0 (0 - mean would
+      // be, times rstd, an infinity where both are large)
+      const float mean = (v * RL + t) * VEC < C ? cur.mean : 0.0f;
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
         const int e = v * VEC + k;
-        const float dy = cur.g[v].get(k), xh = (cur.x[v].get(k) - cur.mean) * cur.rstd, gy = dy * w[e];
+        const float dy = cur.g[v].get(k), xh = (cur.x[v].get(k) - mean) * cur.rstd, gy = dy * w[e];
         s1 = s1 + gy;
         s2 = __builtin_fmaf(gy, xh, s2);
-        // a row past the end has dy = 0 and xh = 0; a column past it is not stored
         dw[e] = __builtin_fmaf(dy, xh, dw[e]);
         db[e] = db[e] + dy;
       }
+    }
     group_sum2<WPR>(s1, s2, red, turn);
     if (a.dx && r < a.R) {
       s1 = s1 * inv;

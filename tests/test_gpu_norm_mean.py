@@ -13,7 +13,7 @@ import torch
 
 import mxfp4_microscaling_quantization_mx_amd as mx
 from gpu_util import banner, host, need_gpu
-from test_gpu_norm import BF, F32, U, f64, near, strided
+from test_gpu_norm import BF, F32, U, backward, f64, near, strided
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,23 @@ def test_bf16_means_far_above_the_spread():
     near(host(y.float()), ry, ty, "y", True)
     near(host(mean), rm, tm, "mean")
     near(host(rstd), rr, tr, "rstd")
+
+
+@pytest.mark.parametrize("C", [5, 64, 100, 1111, 2880, 9000])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_backward_of_huge_rows_of_one_value(C, dtype):
+    """mean * rstd is past float32, the centred values are zero: the lanes past
+    the row's end must not bring an infinity into its sums."""
+    need_gpu()
+    rng = np.random.default_rng(C)
+    vals = np.array([2.0 ** 123, -3e38, 1e30, -1e36])
+    x = strided(np.repeat(vals[:, None], C, 1), dtype, 0, 0)
+    dy = strided(rng.standard_normal((len(vals), C)), dtype, 0, 0)
+    w = torch.from_numpy((1 + 0.1 * rng.standard_normal(C)).astype(np.float32)).cuda()
+    banner(f"norm backward of huge rows C={C} {dtype}")
+    _, mean, rstd = mx.layer_norm(x, w)
+    got = mx.layer_norm_backward(dy, x, mean, rstd, w)
+    ref, tol = backward(f64(dy), f64(x), f64(mean), f64(rstd), f64(w))
+    near(host(got[0].float()), ref[0], tol[0], "dx", dtype == BF)
+    near(host(got[1]), ref[1], tol[1], "dweight")
+    near(host(got[2]), ref[2], tol[2], "dbias")
