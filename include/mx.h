@@ -519,9 +519,11 @@ mx_status mx_gemm_gated(const mx_tensor* A, const mx_tensor* B, const mx_gate_cf
  *   dg = dH * (clamp(u) + up_shift) * act'(min(g, limit)) * [g <= limit]
  *   du = dH * act(min(g, limit)) * [|u| <= limit]
  * with g and u recomputed from A and B in the same kernel (nothing is saved by
- * the forward pass).  dP holds dg and du in the column order that B has rows,
- * so the data and weight gradients are products like any linear layer's:
- * dA = dP B and dB = dP^T A (mx_quantize of dP along either axis, mx_gemm).
+ * the forward pass).  A gradient that a clamp stops is 0 whatever dH holds; NaN
+ * in g or u makes both gradients NaN, stopped or not.  dP holds dg and du in
+ * the column order that B has rows, so the data and weight gradients are
+ * products like any linear layer's: dA = dP B and dB = dP^T A (mx_quantize of
+ * dP along either axis, mx_gemm).
  *
  *   dH     device; [M, N] of dh_dtype, row stride lddh elements (>= N).
  *   dP     device; [M, 2N] of dp_dtype, row stride lddp elements (>= 2N).

@@ -83,12 +83,16 @@ __device__ __forceinline__ float gate_forward(const GateP& p, float g, float u) 
   return gate_act<ACT, false>(p, gate_low(g, p.limit), d) * (gate_clamp(u, p.limit) + p.shift);
 }
 
+// NaN in either projection makes both gradients NaN, past a clamp too: the zero
+// there is z, NaN where u is (a limit that is passed is finite, and with it the
+// clamped u), and du's takes the factor that is NaN where g is.
 template <int ACT>
 __device__ __forceinline__ void gate_backward(const GateP& p, float g, float u, float dh, float& dg, float& du) {
   float d;
-  const float a = gate_act<ACT, true>(p, gate_low(g, p.limit), d);
-  dg = g > p.limit ? 0.0f : dh * (gate_clamp(u, p.limit) + p.shift) * d;
-  du = __builtin_fabsf(u) > p.limit ? 0.0f : dh * a;
+  const float a = gate_act<ACT, true>(p, gate_low(g, p.limit), d), c = gate_clamp(u, p.limit);
+  const float z = c - c;
+  dg = g > p.limit ? z : dh * (c + p.shift) * d;
+  du = __builtin_fabsf(u) <= p.limit ? dh * a : z * a;
 }
 
 // The same with the activation chosen at run time.
