@@ -95,14 +95,4 @@ __device__ __forceinline__ void gate_backward(const GateP& p, float g, float u, 
   du = __builtin_fabsf(u) <= p.limit ? dh * a : z * a;
 }
 
-// The same with the activation chosen at run time.
-__device__ __forceinline__ float gate_forward_any(const GateP& p, float g, float u) {
-  return p.act == 0 ? gate_forward<0>(p, g, u) : p.act == 1 ? gate_forward<1>(p, g, u) : gate_forward<2>(p, g, u);
-}
-__device__ __forceinline__ void gate_backward_any(const GateP& p, float g, float u, float dh, float& dg, float& du) {
-  if (p.act == 0) gate_backward<0>(p, g, u, dh, dg, du);
-  else if (p.act == 1) gate_backward<1>(p, g, u, dh, dg, du);
-  else gate_backward<2>(p, g, u, dh, dg, du);
-}
-
 }  // namespace mx
