@@ -501,6 +501,9 @@ typedef struct {
  *   H[m, n] = act(min(g, limit)) * (clamp(u, -limit, limit) + up_shift),
  * so P never reaches memory.  The formula is evaluated in float32 and rounded
  * once to h_dtype; NaN in an operand makes its outputs NaN (a clamp keeps it).
+ * In units of 2^-24 the sigmoid of SiLU and of the tanh form errs by at most 6 +
+ * 2 |z| and 6 + 4 |z| of itself (z its argument), GELU's normal distribution
+ * function below zero by 11 + 1.25 g^2 of itself.
  *
  *   A, B   host structs of device buffers, as mx_gemm: any element types, 1-D
  *          or 2-D scales; B->rows = 2N must be even.
