@@ -490,6 +490,11 @@ def _check_rows(t, what, shape=None, dtype=None):
         raise ValueError(f"{what} must be {dtype}")
 
 
+def _ld(t):
+    # (one row: its stride means nothing and may be anything)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
 def _gated(what, a, b, gate, out, out_dtype, dh, offsets):
     lib = load_library()
     st = _stream(a.codes, a.scales, b.codes, b.scales, offsets, dh, out)
@@ -512,10 +517,10 @@ def _gated(what, a, b, gate, out, out_dtype, dh, offsets):
     args = ()
     if backward:
         _check_rows(dh, f"{what}: dh", (a.rows, N))
-        args = (_ptr(dh), _DTYPE[dh.dtype], dh.stride(0))
+        args = (_ptr(dh), _DTYPE[dh.dtype], _ld(dh))
     at, gc = a.c_struct(), gate.c_struct()
     _check(getattr(lib, what)(ctypes.byref(at), *group, ctypes.byref(gc), *args, _ptr(out), _DTYPE[out.dtype],
-                              out.stride(0), st))
+                              _ld(out), st))
     return out
 
 
@@ -570,8 +575,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None):
         _check_rows(out, "layer_norm: out", x.shape, x.dtype)
     mean, rstd = x.new_empty(R, dtype=torch.float32), x.new_empty(R, dtype=torch.float32)
     wd = weight if weight is not None else bias
-    _check(lib.mx_layer_norm(_ptr(x), _DTYPE[x.dtype], R, C, x.stride(0), _ptr(weight), _ptr(bias),
-                             MX_DT_F32 if wd is None else _DTYPE[wd.dtype], eps, _ptr(out), out.stride(0),
+    _check(lib.mx_layer_norm(_ptr(x), _DTYPE[x.dtype], R, C, _ld(x), _ptr(weight), _ptr(bias),
+                             MX_DT_F32 if wd is None else _DTYPE[wd.dtype], eps, _ptr(out), _ld(out),
                              _ptr(mean), _ptr(rstd), st))
     return out, mean, rstd
 
@@ -600,8 +605,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, param_dtype=No
     dweight, dbias = x.new_empty(C, dtype=param_dtype), x.new_empty(C, dtype=param_dtype)
     nbytes = lib.mx_layer_norm_backward_workspace_size(R, C)
     ws = x.new_empty(nbytes, dtype=torch.uint8)
-    _check(lib.mx_layer_norm_backward(_ptr(dy), _ptr(x), _DTYPE[x.dtype], R, C, dy.stride(0), x.stride(0), _ptr(mean),
-                                      _ptr(rstd), _ptr(weight), _DTYPE[param_dtype], _ptr(out), out.stride(0),
+    _check(lib.mx_layer_norm_backward(_ptr(dy), _ptr(x), _DTYPE[x.dtype], R, C, _ld(dy), _ld(x), _ptr(mean),
+                                      _ptr(rstd), _ptr(weight), _DTYPE[param_dtype], _ptr(out), _ld(out),
                                       _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes, st))
     return out, dweight, dbias
 
@@ -617,13 +622,13 @@ def dropout(x, p, seed=0, offset=0, residual=None, out=None):
     ldr = 0
     if residual is not None:
         _check_rows(residual, "dropout: residual", x.shape, x.dtype)
-        ldr = residual.stride(0)
+        ldr = _ld(residual)
     if out is None:
         out = x.new_empty((R, C))
     else:
         _check_rows(out, "dropout: out", x.shape, x.dtype)
-    _check(lib.mx_dropout(_ptr(x), _DTYPE[x.dtype], R, C, x.stride(0), p, seed & (2**64 - 1), offset & (2**64 - 1),
-                          _ptr(residual), ldr, _ptr(out), out.stride(0), st))
+    _check(lib.mx_dropout(_ptr(x), _DTYPE[x.dtype], R, C, _ld(x), p, seed & (2**64 - 1), offset & (2**64 - 1),
+                          _ptr(residual), ldr, _ptr(out), _ld(out), st))
     return out
 
 

@@ -149,3 +149,29 @@ def test_offsets_that_are_not_a_plain_int32_list_are_refused(name, offsets):
         args += (at(f32(32, 32), 0),)
     with pytest.raises(ValueError, match="offsets"):
         getattr(mx, name)(*args, **kw)
+
+
+@pytest.mark.parametrize("name", ["layer_norm", "layer_norm_backward", "dropout", "gemm_gated_backward"])
+def test_one_row_may_have_any_row_stride(name, monkeypatch):
+    """A column taken as one row (stride 1, 1) is contiguous: its row stride
+    leads nowhere, and must not be held against it."""
+    seen = []
+    lib = type("Recorder", (StubLibrary,), {"mx_last_error": lambda self: b"",
+                                            "mx_" + name: lambda self, *args: seen.append(args) or 0})()
+    monkeypatch.setattr(mx, "_lib", lib)
+    monkeypatch.setattr(torch.Tensor, "new_empty", torch.Tensor.new_zeros)   # (keeps to the host)
+    row = lambda n: at(f32(n, 1).t(), 0)
+    assert row(32).stride() == (1, 1) and row(32).is_contiguous()
+    if name == "layer_norm":
+        mx.layer_norm(row(32), out=row(32))
+        strides = [(seen[0][4], 32), (seen[0][10], 32)]
+    elif name == "layer_norm_backward":
+        mx.layer_norm_backward(row(32), row(32), at(f32(1), 0), at(f32(1), 0), out=row(32))
+        strides = [(seen[0][i], 32) for i in (5, 6, 12)]
+    elif name == "dropout":
+        mx.dropout(row(32), 0.1, residual=row(32), out=row(32))
+        strides = [(seen[0][i], 32) for i in (4, 9, 11)]
+    else:
+        mx.gemm_gated_backward(mxt(1, 0), mxt(48, 0), row(24), out=row(48))
+        strides = [(seen[0][5], 24), (seen[0][8], 48)]
+    assert all(ld >= n for ld, n in strides), strides

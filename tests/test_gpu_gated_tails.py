@@ -69,7 +69,7 @@ def reference(x, gate):
     s = 0.5 * (1 + np.tanh(z / 2))
     s = np.where(z < 0, np.exp(z - np.log1p(np.exp(np.minimum(z, 0)))), s)
     ts = s * (6 + per * np.abs(z)) * U
-    a, one = x * s, 1 / (1 + np.exp(z))                     # 1 - s
+    a, one = x * s, 1 / (1 + np.exp(np.minimum(z, 700)))                     # 1 - s
     d = s + a * one * dz
     # 1 - s is a float32 subtraction from 1: off by s's error and one rounding
     td = ts + np.abs(x * dz) * (ts * one + s * (ts + U)) + np.abs(a * one * dz) * 6 * U + np.abs(d) * U
