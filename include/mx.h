@@ -488,7 +488,8 @@ typedef enum {
 typedef struct {
   int32_t act;      /* mx_act                                                  */
   int32_t layout;   /* mx_gate_layout                                          */
-  float alpha;      /* slope of the SiLU's sigmoid (finite, > 0); 1 = plain    */
+  float alpha;      /* slope of the SiLU's sigmoid (finite, > 0); 1 = plain;
+                       the GELUs have none and ignore it                       */
   float limit;      /* clamp of the projections (>= 0); 0 = none               */
   float up_shift;   /* added to the clamped up projection (finite)             */
 } mx_gate_cfg;

@@ -465,14 +465,19 @@ def grouped_gemm_quantize(a, offsets, b, scale_mode="floor", out=None):
 class Gate:
     """A gated block: act(min(g, limit)) * (clamp(u, -limit, limit) + up_shift)
     for the gate and up projections g, u (mx_gate_cfg in include/mx.h).  act:
-    "silu" (g * sigmoid(alpha g)), "gelu" or "gelu_tanh"; limit None: no
-    clamp.  layout: gate and up rows of the weight "interleaved" or in two
-    "halves" (gates first)."""
+    "silu" (g * sigmoid(alpha g)), "gelu" or "gelu_tanh" (which have no alpha
+    and ignore it); limit None: no clamp.  layout: gate and up rows of the
+    weight "interleaved" or in two "halves" (gates first)."""
     act: str = "silu"
     alpha: float = 1.0
     limit: float = None
     up_shift: float = 0.0
     layout: str = "interleaved"
+
+    def __post_init__(self):
+        # the library's 0 is no clamp
+        if self.limit is not None and ctypes.c_float(self.limit).value == 0.0:
+            raise ValueError("Gate: a limit of 0 cannot be expressed (None: no clamp)")
 
     def c_struct(self):
         return GateCfgC(_ACT[self.act], _GATE_LAYOUT[self.layout], self.alpha,

@@ -175,3 +175,17 @@ def test_one_row_may_have_any_row_stride(name, monkeypatch):
         mx.gemm_gated_backward(mxt(1, 0), mxt(48, 0), row(24), out=row(48))
         strides = [(seen[0][5], 24), (seen[0][8], 48)]
     assert all(ld >= n for ld, n in strides), strides
+
+
+@pytest.mark.parametrize("limit", [0.0, -0.0, 0])
+def test_a_limit_of_zero_is_refused(limit):
+    """0 is the C interface's "no clamp"; a clamp at zero must not turn into none."""
+    with pytest.raises(ValueError, match="limit"):
+        mx.Gate(limit=limit)
+    assert mx.Gate(limit=None).c_struct().limit == 0.0 and mx.Gate(limit=7.0).c_struct().limit == 7.0
+
+
+def test_a_limit_below_float32_is_refused():
+    """It would reach the library as 0, no clamp."""
+    with pytest.raises(ValueError, match="limit"):
+        mx.Gate(limit=1e-60)
