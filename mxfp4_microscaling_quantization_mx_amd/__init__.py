@@ -579,6 +579,9 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None):
     else:
         _check_rows(out, "layer_norm: out", x.shape, x.dtype)
     mean, rstd = x.new_empty(R, dtype=torch.float32), x.new_empty(R, dtype=torch.float32)
+    if not C:                                   # (the library writes nothing then)
+        mean.fill_(float("nan"))
+        rstd.fill_(float("nan"))
     wd = weight if weight is not None else bias
     _check(lib.mx_layer_norm(_ptr(x), _DTYPE[x.dtype], R, C, _ld(x), _ptr(weight), _ptr(bias),
                              MX_DT_F32 if wd is None else _DTYPE[wd.dtype], eps, _ptr(out), _ld(out),

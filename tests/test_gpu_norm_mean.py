@@ -110,3 +110,15 @@ def test_backward_of_huge_rows_of_one_value(C, dtype):
     near(host(got[0].float()), ref[0], tol[0], "dx", dtype == BF)
     near(host(got[1]), ref[1], tol[1], "dweight")
     near(host(got[2]), ref[2], tol[2], "dbias")
+
+
+def test_rows_without_columns():
+    """The mean of nothing is NaN, not what the memory held."""
+    need_gpu()
+    banner("norm no columns")
+    stale = [torch.full((5,), 3.0, device="cuda") for _ in range(2)]
+    del stale
+    y, mean, rstd = mx.layer_norm(torch.empty(5, 0, device="cuda"))
+    assert y.shape == (5, 0) and mean.isnan().all() and rstd.isnan().all()
+    dx, dw, db = mx.layer_norm_backward(y, y, mean, rstd)
+    assert dx.shape == (5, 0) and dw.shape == db.shape == (0,)
