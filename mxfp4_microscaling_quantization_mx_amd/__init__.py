@@ -173,10 +173,11 @@ class MXTensor:
     elem: str = "e2m1"
 
     def c_struct(self):
+        elem, bits = _ELEM[self.elem]
+        codes, scales = self.codes.stride(), self.scales.stride()
         return MxTensorC(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.K,
-                         self.codes.stride(0) if self.codes.dim() == 2 else self.K * _ELEM[self.elem][1] // 8,
-                         self.scales.stride(0) if self.scales.dim() == 2 else self.K // 32,
-                         _BLOCK[self.block], _ELEM[self.elem][0])
+                         codes[0] if len(codes) == 2 else self.K * bits // 8,
+                         scales[0] if len(scales) == 2 else self.K // 32, _BLOCK[self.block], elem)
 
 
 def empty_mx(rows, K, block="1d", device="cuda", experts=None, elem="e2m1"):
@@ -485,19 +486,19 @@ class Gate:
 
 
 def _check_rows(t, what, shape=None, dtype=None):
-    if t.dim() != 2 or t.dtype not in _DTYPE or not t.is_cuda:
+    """The row stride of a row-major matrix (where it is: _stream).  One row's
+    stride means nothing and may be anything."""
+    st = t.stride()
+    if len(st) != 2 or t.dtype not in _DTYPE:
         raise ValueError(f"{what} must be a 2-D bf16/float32 CUDA tensor")
-    if t.stride(1) != 1 and t.shape[1] > 1:
+    R, C = t.shape
+    if st[1] != 1 and C > 1:
         raise ValueError(f"{what} must be row-major (stride(1) == 1)")
-    if shape is not None and t.shape != shape:
+    if shape is not None and (R, C) != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype}")
-
-
-def _ld(t):
-    # (one row: its stride means nothing and may be anything)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return st[0] if R > 1 else C
 
 
 def _gated(what, a, b, gate, out, out_dtype, dh, offsets):
@@ -516,16 +517,16 @@ def _gated(what, a, b, gate, out, out_dtype, dh, offsets):
     N = rows // 2
     shape = (a.rows, rows if backward else N)
     if out is None:
-        out = a.codes.new_empty(shape, dtype=out_dtype)
+        out, ldo = a.codes.new_empty(shape, dtype=out_dtype), shape[1]
     else:
-        _check_rows(out, f"{what}: out", shape)
+        ldo = _check_rows(out, f"{what}: out", shape)
     args = ()
     if backward:
-        _check_rows(dh, f"{what}: dh", (a.rows, N))
-        args = (_ptr(dh), _DTYPE[dh.dtype], _ld(dh))
+        ldh = _check_rows(dh, f"{what}: dh", (a.rows, N))
+        args = (_ptr(dh), _DTYPE[dh.dtype], ldh)
     at, gc = a.c_struct(), gate.c_struct()
     _check(getattr(lib, what)(ctypes.byref(at), *group, ctypes.byref(gc), *args, _ptr(out), _DTYPE[out.dtype],
-                              _ld(out), st))
+                              ldo, st))
     return out
 
 
@@ -567,7 +568,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None):
     mx_layer_norm): (y, mean, rstd), the row statistics in float32 for
     layer_norm_backward."""
     lib = load_library()
-    _check_rows(x, "layer_norm: x")
+    ldx = _check_rows(x, "layer_norm: x")
     st = _stream(x, weight, bias, out)
     R, C = x.shape
     if weight is not None:
@@ -575,16 +576,16 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None):
     if bias is not None:
         _norm_param(bias, C, None if weight is None else weight.dtype, "layer_norm: bias")
     if out is None:
-        out = x.new_empty((R, C))
+        out, ldo = x.new_empty((R, C)), C
     else:
-        _check_rows(out, "layer_norm: out", x.shape, x.dtype)
+        ldo = _check_rows(out, "layer_norm: out", (R, C), x.dtype)
     mean, rstd = x.new_empty(R, dtype=torch.float32), x.new_empty(R, dtype=torch.float32)
     if not C:                                   # (the library writes nothing then)
         mean.fill_(float("nan"))
         rstd.fill_(float("nan"))
     wd = weight if weight is not None else bias
-    _check(lib.mx_layer_norm(_ptr(x), _DTYPE[x.dtype], R, C, _ld(x), _ptr(weight), _ptr(bias),
-                             MX_DT_F32 if wd is None else _DTYPE[wd.dtype], eps, _ptr(out), _ld(out),
+    _check(lib.mx_layer_norm(_ptr(x), _DTYPE[x.dtype], R, C, ldx, _ptr(weight), _ptr(bias),
+                             MX_DT_F32 if wd is None else _DTYPE[wd.dtype], eps, _ptr(out), ldo,
                              _ptr(mean), _ptr(rstd), st))
     return out, mean, rstd
 
@@ -594,10 +595,10 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, param_dtype=No
     mx_layer_norm_backward).  dweight and dbias have the weight's dtype, or
     param_dtype without one (default float32); out receives dx."""
     lib = load_library()
-    _check_rows(x, "layer_norm_backward: x")
-    _check_rows(dy, "layer_norm_backward: dy", x.shape, x.dtype)
-    st = _stream(x, dy, mean, rstd, weight, out)
+    ldx = _check_rows(x, "layer_norm_backward: x")
     R, C = x.shape
+    lddy = _check_rows(dy, "layer_norm_backward: dy", (R, C), x.dtype)
+    st = _stream(x, dy, mean, rstd, weight, out)
     for t, n in ((mean, "mean"), (rstd, "rstd")):
         if t.shape != (R,) or t.dtype != torch.float32 or not t.is_cuda or (R > 1 and t.stride(0) != 1):
             raise ValueError(f"layer_norm_backward: {n} must be a contiguous float32 CUDA tensor of {R} entries")
@@ -607,14 +608,14 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, param_dtype=No
     elif param_dtype is None:
         param_dtype = torch.float32
     if out is None:
-        out = x.new_empty((R, C))
+        out, lddx = x.new_empty((R, C)), C
     else:
-        _check_rows(out, "layer_norm_backward: out", x.shape, x.dtype)
+        lddx = _check_rows(out, "layer_norm_backward: out", (R, C), x.dtype)
     dweight, dbias = x.new_empty(C, dtype=param_dtype), x.new_empty(C, dtype=param_dtype)
     nbytes = lib.mx_layer_norm_backward_workspace_size(R, C)
     ws = x.new_empty(nbytes, dtype=torch.uint8)
-    _check(lib.mx_layer_norm_backward(_ptr(dy), _ptr(x), _DTYPE[x.dtype], R, C, _ld(dy), _ld(x), _ptr(mean),
-                                      _ptr(rstd), _ptr(weight), _DTYPE[param_dtype], _ptr(out), _ld(out),
+    _check(lib.mx_layer_norm_backward(_ptr(dy), _ptr(x), _DTYPE[x.dtype], R, C, lddy, ldx, _ptr(mean),
+                                      _ptr(rstd), _ptr(weight), _DTYPE[param_dtype], _ptr(out), lddx,
                                       _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes, st))
     return out, dweight, dbias
 
@@ -624,19 +625,18 @@ def dropout(x, p, seed=0, offset=0, residual=None, out=None):
     optional residual (see mx_dropout).  The backward pass is this call on the
     gradient with the same p, seed and offset and no residual."""
     lib = load_library()
-    _check_rows(x, "dropout: x")
+    ldx = _check_rows(x, "dropout: x")
     st = _stream(x, residual, out)
     R, C = x.shape
     ldr = 0
     if residual is not None:
-        _check_rows(residual, "dropout: residual", x.shape, x.dtype)
-        ldr = _ld(residual)
+        ldr = _check_rows(residual, "dropout: residual", (R, C), x.dtype)
     if out is None:
-        out = x.new_empty((R, C))
+        out, ldo = x.new_empty((R, C)), C
     else:
-        _check_rows(out, "dropout: out", x.shape, x.dtype)
-    _check(lib.mx_dropout(_ptr(x), _DTYPE[x.dtype], R, C, _ld(x), p, seed & (2**64 - 1), offset & (2**64 - 1),
-                          _ptr(residual), ldr, _ptr(out), _ld(out), st))
+        ldo = _check_rows(out, "dropout: out", (R, C), x.dtype)
+    _check(lib.mx_dropout(_ptr(x), _DTYPE[x.dtype], R, C, ldx, p, seed & (2**64 - 1), offset & (2**64 - 1),
+                          _ptr(residual), ldr, _ptr(out), ldo, st))
     return out
 
 
