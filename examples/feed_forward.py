@@ -9,9 +9,10 @@ residual; then every gradient.  The backward products follow the library's
 MXFP4 recipe: gradients quantized with stochastic rounding, the data gradients
 through the exact transposes of the forward weights, the weight gradients from
 both operands quantized along the token dimension with the randomized Hadamard
-transform.  Nothing but x, the normalized rows' quantization, the block's
-output and the norm's statistics is kept for the backward pass: the gated
-block recomputes its projections and the dropout mask comes from its seed.
+transform.  Kept for the backward pass are x, the normalized rows (bf16, for the
+weight gradient, and quantized), the block's output, the norm's statistics and
+the quantized weights: the gated block recomputes its projections and the
+dropout mask comes from its seed.
 
     python examples/feed_forward.py            # train on a fixed batch, then serve one token
 """

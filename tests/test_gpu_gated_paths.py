@@ -19,7 +19,8 @@ TIGHT_HALVES = mx.Gate("silu", 1.702, 1.25, 1.0, "halves")
 # element types of A and B, rows, hidden columns
 PATHS = {
     "few, 8 waves": ("e2m1", "e2m1", 20, 24),
-    "few, 2 waves": ("e4m3", "e2m1", 100, 2881),
+    "few, 2 waves": ("e2m1", "e2m1", 100, 2881),
+    "tiles, mixed, one row of tiles": ("e4m3", "e2m1", 100, 2881),
     "tiles, MXFP4": ("e2m1", "e2m1", 420, 900),
     "tiles, MXFP8": ("e4m3", "e4m3", 420, 900),
     "tiles, mixed": ("e4m3", "e2m1", 420, 900),
