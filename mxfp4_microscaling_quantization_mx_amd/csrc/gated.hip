@@ -614,7 +614,10 @@ hipError_t launch_direct_b(const GatedArgs& a, bool few, hipStream_t st) {
 //    from HBM, up to 8 rows per expert (32 experts, 64 rows 43 against the
 //    pipeline's 68, 256 rows 70 / 78, 512 rows about 90 / 83; MXFP8 95 / 140, 136
 //    / 147) or 6 workgroups per CU (512 x 1024: 512 rows 11 / 15, 1024 rows 15 /
-//    15).
+//    15).  Wide weights (K = 4096, out of the caches) leave it: with 32 rows of
+//    14336 columns it takes 29 against k_gated_tile's 21, with 32 of 28672 50
+//    against the pipeline's 35 (MXFP8 82 / 65); with a single row 20 / 22 and 35 /
+//    36 (MXFP8 33 / 31, 11008 columns 23 / 27).
 //  * k_gated_tile while one workgroup per CU does in MXFP4, 16-18 against the
 //    21-24 of a pipeline that is not full and 32 with two; while two do with
 //    wider elements, 22-24 with one, 43 with two against the pipeline's 47-49

@@ -11,15 +11,16 @@
 // Forward 16384 x 2880 x 2880: 151-155 us, 3.5-3.6 PFLOP/s; the plain product of
 // the same operands with bf16 output takes 174 on the same card, its epilogue
 // writing twice the bytes.  The MFMA pipeline bounds it: 123 us with no
-// epilogue at all.  Backward: 208 us, 316 MB moved; without its stores 35 us
+// epilogue at all.  Backward: 201-204 us, 316 MB moved; without its stores 35 us
 // less, without the reads of dH 28, without the derivatives 24, without all
-// three 127.  What remains of the epilogue is not hidden since one workgroup
+// three 127 (of 208 then).  What remains of the epilogue is not hidden since one workgroup
 // fills a CU's registers and all reach their tile ends together; starting the
 // workgroups in 2 to 8 phases changed nothing, nor did bringing dH into L2 a
 // stage ahead, nor loading the next tile's second stage before the stores.
-// Grouped, 65536 rows over 32 experts: 651 us, 3.3 PFLOP/s; backward of 16384
-// rows over 32 experts 261-288, of which ragged row tiles take a quarter (80
-// row tiles of 256 for 64 full ones' rows).
+// Grouped, 65536 rows over 32 experts: 634-654 us, 3.3-3.4 PFLOP/s; backward of
+// 16384 rows over 32 experts 260-291, of which ragged row tiles take a quarter
+// (80 row tiles of 256 for 64 full ones' rows); its kernels spill 10-11 VGPRs
+// (44-52 bytes of scratch per lane; the dense ones 3-5, forward none).
 #define MX_T256_NS t256
 #define MX_T256_SWAP 0
 #include "gemm_tile256.h"

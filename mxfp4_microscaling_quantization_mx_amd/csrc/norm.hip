@@ -25,7 +25,9 @@
 //    workgroup's row groups are added through LDS at the end and stored as one
 //    partial row [2][C].  16384 x 2880 bf16: 51 us, 5.6 TB/s (72 us with one
 //    wave per row, the weights read again and no row ahead), 57 with the sum of
-//    the partial rows; 4099 x 1111 float32, unaligned: 16 us, 3.5 TB/s.
+//    the partial rows.  Rows that no 16-byte piece fits are read element by
+//    element, the same number of loads whatever their size: 4099 x 1111 15.4 us
+//    in float32 (3.5 TB/s), 33.6 in bf16 (0.8), forward 9.5 and 12.8.
 //  * k_norm_any, k_norm_dx_any, k_norm_dw_any: rows too long for registers,
 //    read once per sum (the later reads come from cache), the weight's
 //    gradient by columns.
@@ -550,13 +552,14 @@ __global__ __launch_bounds__(1024) void k_norm_dw_sum(const float* __restrict__ 
   }
 }
 
-// Partial rows of dw and db: workgroups of k_norm_backward (one per CU) and row
-// groups of k_norm_dw_any.
 // Workgroups of k_norm per CU: 16384 x 2880 bf16 41.6 us with 1, 37.7 with 2,
-// 41.2 with 3; single elements per lane need more waves (4099 x 1111 bf16 13.5
-// us with 2, 9.8 with 3, 9.2 with 4, 10.7 with 8).
+// 41.2 with 3; single elements per lane need more waves (4099 x 1111 bf16 on
+// inputs in the caches 13.5 us with 2, 9.8 with 3, 9.2 with 4, 10.7 with 8).
 template <int VEC>
 constexpr int64_t norm_per_cu() { return VEC == 1 ? 4 : 2; }
+// Most partial rows of dw and db: workgroups of k_norm_backward (one for each of
+// the 256 CUs) and row groups of k_norm_dw_any.  A constant, so that the order of
+// the sums does not follow the card.
 constexpr int64_t MOST_GROUPS = 256;
 int64_t norm_groups(int64_t R) { return R < MOST_GROUPS ? R : MOST_GROUPS; }
 

@@ -67,7 +67,7 @@ def reference(x, gate):
         c = 2 * np.sqrt(2 / np.pi)
         z, dz, per = c * (x + 0.044715 * x ** 3), c * (1 + 3 * 0.044715 * x * x), 4
     s = 0.5 * (1 + np.tanh(z / 2))
-    s = np.where(z < 0, np.exp(z - np.log1p(np.exp(np.minimum(z, 0)))), s)
+    s = np.where(z < 0, np.exp(np.minimum(z, 0) - np.log1p(np.exp(np.minimum(z, 0)))), s)
     ts = s * (6 + per * np.abs(z)) * U
     a, one = x * s, 1 / (1 + np.exp(np.minimum(z, 700)))                     # 1 - s
     d = s + a * one * dz
