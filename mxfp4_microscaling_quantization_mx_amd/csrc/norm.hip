@@ -26,8 +26,9 @@
 //    partial row [2][C].  16384 x 2880 bf16: 51 us, 5.6 TB/s (72 us with one
 //    wave per row, the weights read again and no row ahead), 57 with the sum of
 //    the partial rows.  Rows that no 16-byte piece fits are read element by
-//    element, the same number of loads whatever their size: 4099 x 1111 15.4 us
-//    in float32 (3.5 TB/s), 33.6 in bf16 (0.8), forward 9.5 and 12.8.
+//    element, as many loads in bf16 as in float32 and slower ones: 4099 x 1111
+//    with a weight 17.9 us in float32 (3.1 TB/s; 15.4 without), 33.6 in bf16
+//    (0.8); forward 9.5 and 12.8.
 //  * k_norm_any, k_norm_dx_any, k_norm_dw_any: rows too long for registers,
 //    read once per sum (the later reads come from cache), the weight's
 //    gradient by columns.
