@@ -623,6 +623,160 @@ size_t mx_layer_norm_backward_workspace_size(int64_t R, int64_t C);
 mx_status mx_dropout(const void* x, int32_t dtype, int64_t R, int64_t C, int64_t ldx, float p, uint64_t seed,
                      uint64_t offset, const void* residual, int64_t ldr, void* y, int64_t ldy, void* stream);
 
+/* ------------------------------------------------------------------ expert layer
+ * What stands around the grouped products of an MoE layer ("MXFP4", AI Wiki,
+ * §Use in models): the router, its slots sorted by expert (the inputs of
+ * mx_quantize_gather, mx_quantize_scatter and the grouped products) and the
+ * weighted sum back, each with its gradient.  A slot is a pair (token t, choice
+ * j), 0 <= j < top; [T, top] arrays are contiguous. */
+
+typedef enum { MX_SCORE_SOFTMAX = 0, MX_SCORE_SIGMOID = 1 } mx_score;
+
+typedef struct {
+  int32_t score;        /* mx_score                                              */
+  int32_t renormalize;  /* 1: the chosen scores of a token are divided by their sum */
+  float scale;          /* the weights are multiplied by this (finite)           */
+} mx_router_cfg;
+
+/*
+ * mx_route — the `top` experts of every token and their weights from the logits
+ * l [T, E]: the largest logits, largest first, ties to the lowest index, the
+ * zeros equal, NaN above every number; ids[t, j] is the j-th.  The experts of a
+ * token are distinct.  With the scores
+ *   softmax  s_e = e^(l_e - m) / sum over all experts of e^(l - m),
+ *   sigmoid  s_e = 1 / (1 + e^-l_e),
+ * weights[t, j] = scale * s_e, or renormalized scale * s_e / (sum of the chosen s)
+ * (for softmax the softmax of the chosen logits).  Computed in float32: a weight
+ * errs by at most (32 + ln E + d) 2^-24 of itself, d the distance of its logit from
+ * the token's largest.  Where the largest logit is -Inf (a token that may go
+ * nowhere) the weights are 0, whatever the ids; other -Inf logits have weight 0.
+ * NaN among the logits that a sum takes, or +Inf in a softmax, makes the token's
+ * weights NaN; a NaN logit's own weight is NaN.
+ *
+ *   logits   device; [T, E] of `dtype` (mx_dtype), row stride ld elements (>= E).
+ *   E        1 .. 1024; top 1 .. min(E, 64) (above 64 or 1024: MX_ERR_UNSUPPORTED).
+ *   ids      device; int32 [T, top].  weights: device; float32 [T, top].
+ *   T = 0: nothing is written.  At most 2^31 - 1 tokens.
+ */
+mx_status mx_route(const void* logits, int32_t dtype, int64_t T, int32_t E, int64_t ld, int32_t top,
+                   const mx_router_cfg* cfg, int32_t* ids, float* weights, void* stream);
+
+/*
+ * mx_route_backward — the gradient of mx_route's weights by the logits, for the
+ * choice ids (which is constant), recomputed from the logits: with p_j =
+ * weights[t, j] / scale and D = sum_j p_j dweights[t, j]
+ *   softmax renormalized  dl_j = scale p_j (dw_j - D), 0 for the others,
+ *   softmax               dl_e = scale s_e ([e chosen] dw - D) for every e,
+ *   sigmoid               dl_j = scale dw_j s_j (1 - s_j), 0 for the others,
+ *   sigmoid renormalized  dl_j = scale p_j (1 - s_j) (dw_j - D), 0 for the others.
+ * An id outside [0, E) takes no part; the gradients of one named twice add up.
+ * Tokens whose weights are 0 for want of a finite logit get zeros.
+ *
+ *   dweights  device; float32 [T, top].  ids: device; int32 [T, top].
+ *   dlogits   device; [T, E] of `dtype`, row stride ldd (>= E); every element is
+ *             written.  Must not overlap logits.
+ */
+mx_status mx_route_backward(const float* dweights, const void* logits, int32_t dtype, int64_t T, int32_t E, int64_t ld,
+                            const int32_t* ids, int32_t top, const mx_router_cfg* cfg, void* dlogits, int64_t ldd,
+                            void* stream);
+
+/*
+ * mx_expert_sort — the slots sorted by expert, in slot order within an expert (a
+ * stable sort; the same result on every run):
+ *   offsets[e]   first sorted row of expert e, offsets[E] the number of rows
+ *                (the d_group_offsets of the grouped products);
+ *   rows[i]      the token of sorted row i (the `rows` of mx_quantize_gather), -1
+ *                from offsets[E] on;
+ *   dest[t, j]   the sorted row of a slot (the `dest` of mx_quantize_scatter and of
+ *                the calls below).
+ * A slot whose id is outside [0, E) is dropped: dest -1, no row.
+ *
+ *   ids        device; int32 [T, top], 4-byte aligned.  top >= 1, E 1 .. 1024 (above:
+ *              MX_ERR_UNSUPPORTED), at most 2^31 - 1 slots.
+ *   offsets    device; int32 [E + 1].  rows: device; int32 [T * top]; dest: device;
+ *              int32 [T, top].  None may overlap ids or each other.
+ *   workspace  device, 4-byte aligned, mx_expert_sort_workspace_size(T, top, E)
+ *              bytes (NULL where that is 0); contents before and after are of no
+ *              meaning.
+ *   T = 0: offsets are zeros.
+ */
+mx_status mx_expert_sort(const int32_t* ids, int64_t T, int32_t top, int32_t E, int32_t* offsets, int32_t* rows,
+                         int32_t* dest, void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace mx_expert_sort needs (0 up to 4096 slots). */
+size_t mx_expert_sort_workspace_size(int64_t T, int32_t top, int32_t E);
+
+/*
+ * mx_expert_dispatch — xs[dest[t, j]] = x[t]: token rows copied to their sorted
+ * rows, unquantized (mx_quantize_scatter quantizes on the way).  Its gradient is
+ * mx_expert_combine of dxs without weights.
+ *
+ *   x     device; [T, C] of `dtype`, row stride ldx (>= C), element-aligned.
+ *   dest  device; int32 [T, top]; entries outside [0, rows) are skipped.
+ *   xs    device; [rows, C] of `dtype`, row stride ldxs (>= C).  Rows that no entry
+ *         names are left untouched; a row named twice gets one of the tokens' bytes in
+ *         each of its pieces.  Must not overlap x.
+ */
+mx_status mx_expert_dispatch(const void* x, int32_t dtype, int64_t T, int64_t C, int64_t ldx, const int32_t* dest,
+                             int32_t top, void* xs, int64_t rows, int64_t ldxs, void* stream);
+
+/*
+ * mx_expert_combine — out[t] = sum_j weights[t, j] * y[dest[t, j]] + residual[t]:
+ * the experts' rows back to their tokens, in float32 in the order of j, rounded
+ * once.  An entry of dest outside [0, rows) adds nothing, whatever its weight.
+ *
+ *   y         device; [rows, C] of `dtype`, row stride ldy (>= C), element-aligned.
+ *   dest      device; int32 [T, top].
+ *   weights   device; float32 [T, top]; NULL = 1 (the gradient of a dispatch).
+ *   residual  device; [T, C] of `dtype`, row stride ldr; NULL = none.
+ *   out       device; [T, C] of `dtype`, row stride ldo.  May be residual itself.
+ */
+mx_status mx_expert_combine(const void* y, int32_t dtype, int64_t rows, int64_t C, int64_t ldy, const int32_t* dest,
+                            const float* weights, int64_t T, int32_t top, const void* residual, int64_t ldr, void* out,
+                            int64_t ldo, void* stream);
+
+/*
+ * mx_expert_combine_backward — the gradients of mx_expert_combine (the residual's
+ * is dout):
+ *   dy[dest[t, j]]  = weights[t, j] * dout[t],
+ *   dweights[t, j]  = sum_c dout[t, c] * y[dest[t, j], c]  (0 for a dropped slot),
+ * in float32, the sum in an order fixed by C and the type: the same bits on every
+ * run.  Rows of dy that no entry names are left untouched; the entries of dest must
+ * be distinct, as mx_expert_sort makes them (a row named twice gets one of its
+ * two gradients in each of its pieces, not their sum).
+ *
+ *   dout  device; [T, C] of `dtype`.  y, dy: device; [rows, C] of `dtype`; dy may be
+ *         y itself (the same base and stride).
+ *   dest  device; int32 [T, top].  weights, dweights: device; float32 [T, top].
+ */
+mx_status mx_expert_combine_backward(const void* dout, int32_t dtype, int64_t T, int64_t C, int64_t lddo,
+                                     const void* y, int64_t rows, int64_t ldy, const int32_t* dest,
+                                     const float* weights, int32_t top, void* dy, int64_t lddy, float* dweights,
+                                     void* stream);
+
+/*
+ * mx_bias_grad, mx_grouped_bias_grad — the sums of the columns of dp [M, N], the
+ * gradient of a bias: over all rows, or over the rows of each expert (offsets and
+ * their clamping as in mx_grouped_gemm; rows past off[E] are not read; an expert
+ * without rows gets zeros).  In float32 in an order fixed by the shape, the
+ * offsets and the types (the same bits on every run), rounded once.
+ *
+ *   dp         device; [M, N] of `dtype`, row stride ld (>= N), element-aligned.
+ *   out        device; [N], or [E, N] contiguous, of out_dtype.
+ *   workspace  device, 4-byte aligned, mx_bias_grad_workspace_size(M, N, E) bytes
+ *              (E = 1 for mx_bias_grad; NULL where that is 0); contents before and
+ *              after are of no meaning.
+ *   N = 0: nothing is written.  M = 0 writes zeros.
+ */
+mx_status mx_bias_grad(const void* dp, int32_t dtype, int64_t M, int64_t N, int64_t ld, void* out, int32_t out_dtype,
+                       void* workspace, size_t ws_bytes, void* stream);
+mx_status mx_grouped_bias_grad(const void* dp, int32_t dtype, int64_t M, int64_t N, int64_t ld,
+                               const int32_t* d_group_offsets, int32_t E, void* out, int32_t out_dtype, void* workspace,
+                               size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace the bias gradients need. */
+size_t mx_bias_grad_workspace_size(int64_t M, int64_t N, int32_t E);
+
 /* Message describing the last failed call on this thread ("" if none). */
 const char* mx_last_error(void);
 

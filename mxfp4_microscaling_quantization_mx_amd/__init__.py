@@ -38,6 +38,7 @@ _SCALE = {"floor": 0, "round_up": 1, "prescale_3_4": 2}
 # MX element types: name -> (mx_elem, bits per element)
 _ELEM = {"e2m1": (0, 4), "e4m3": (1, 8), "e5m2": (2, 8), "e2m3": (3, 6), "e3m2": (4, 6)}
 _ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+_SCORE = {"softmax": 0, "sigmoid": 1}
 _GATE_LAYOUT = {"interleaved": 0, "halves": 1}
 _DTYPE = {torch.float32: MX_DT_F32, torch.bfloat16: MX_DT_BF16}
 
@@ -45,7 +46,9 @@ EXPORTED = ("mx_quantize", "mx_quantize_gather", "mx_quantize_scatter", "mx_dequ
             "mx_gemm_quantize", "mx_gemm_workspace_size", "mx_gemm_noalloc", "mx_gemm_fused_quant_a", "mx_grouped_gemm",
             "mx_grouped_gemm_quantize", "mx_clip_count", "mx_gemm_gated", "mx_gemm_gated_backward",
             "mx_grouped_gemm_gated", "mx_grouped_gemm_gated_backward", "mx_layer_norm", "mx_layer_norm_backward",
-            "mx_layer_norm_backward_workspace_size", "mx_dropout",
+            "mx_layer_norm_backward_workspace_size", "mx_dropout", "mx_route", "mx_route_backward", "mx_expert_sort",
+            "mx_expert_sort_workspace_size", "mx_expert_dispatch", "mx_expert_combine", "mx_expert_combine_backward",
+            "mx_bias_grad", "mx_grouped_bias_grad", "mx_bias_grad_workspace_size",
             "mx_last_error", "mx_version")
 
 
@@ -66,6 +69,10 @@ class QuantCfgC(ctypes.Structure):
 class GateCfgC(ctypes.Structure):
     _fields_ = [("act", ctypes.c_int32), ("layout", ctypes.c_int32), ("alpha", ctypes.c_float),
                 ("limit", ctypes.c_float), ("up_shift", ctypes.c_float)]
+
+
+class RouterCfgC(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class MXError(RuntimeError):
@@ -119,6 +126,22 @@ def load_library(path=LIB_PATH):
     lib.mx_dropout.argtypes = [P, I32, I64, I64, I64, F32, U64, U64, P, I64, P, I64, P]
     for f in ("mx_gemm_gated", "mx_gemm_gated_backward", "mx_grouped_gemm_gated", "mx_grouped_gemm_gated_backward",
               "mx_layer_norm", "mx_layer_norm_backward", "mx_dropout"):
+        getattr(lib, f).restype = ctypes.c_int
+    SZ, PR = ctypes.c_size_t, ctypes.POINTER(RouterCfgC)
+    lib.mx_route.argtypes = [P, I32, I64, I32, I64, I32, PR, P, P, P]
+    lib.mx_route_backward.argtypes = [P, P, I32, I64, I32, I64, P, I32, PR, P, I64, P]
+    lib.mx_expert_sort.argtypes = [P, I64, I32, I32, P, P, P, P, SZ, P]
+    lib.mx_expert_sort_workspace_size.argtypes = [I64, I32, I32]
+    lib.mx_expert_sort_workspace_size.restype = SZ
+    lib.mx_expert_dispatch.argtypes = [P, I32, I64, I64, I64, P, I32, P, I64, I64, P]
+    lib.mx_expert_combine.argtypes = [P, I32, I64, I64, I64, P, P, I64, I32, P, I64, P, I64, P]
+    lib.mx_expert_combine_backward.argtypes = [P, I32, I64, I64, I64, P, I64, I64, P, P, I32, P, I64, P, P]
+    lib.mx_bias_grad.argtypes = [P, I32, I64, I64, I64, P, I32, P, SZ, P]
+    lib.mx_grouped_bias_grad.argtypes = [P, I32, I64, I64, I64, P, I32, P, I32, P, SZ, P]
+    lib.mx_bias_grad_workspace_size.argtypes = [I64, I64, I32]
+    lib.mx_bias_grad_workspace_size.restype = SZ
+    for f in ("mx_route", "mx_route_backward", "mx_expert_sort", "mx_expert_dispatch", "mx_expert_combine",
+              "mx_expert_combine_backward", "mx_bias_grad", "mx_grouped_bias_grad"):
         getattr(lib, f).restype = ctypes.c_int
     lib.mx_last_error.restype = ctypes.c_char_p
     lib.mx_last_error.argtypes = []
@@ -637,6 +660,176 @@ def dropout(x, p, seed=0, offset=0, residual=None, out=None):
         ldo = _check_rows(out, "dropout: out", (R, C), x.dtype)
     _check(lib.mx_dropout(_ptr(x), _DTYPE[x.dtype], R, C, ldx, p, seed & (2**64 - 1), offset & (2**64 - 1),
                           _ptr(residual), ldr, _ptr(out), ldo, st))
+    return out
+
+
+@dataclass(frozen=True)
+class Router:
+    """How routing weights come from logits (mx_router_cfg in include/mx.h).
+    score: "softmax" or "sigmoid"; renormalize: the chosen scores of a token are
+    divided by their sum; scale: a factor of every weight."""
+    score: str = "softmax"
+    renormalize: bool = True
+    scale: float = 1.0
+
+    def c_struct(self):
+        return RouterCfgC(_SCORE[self.score], int(self.renormalize), self.scale)
+
+
+def _slots(t, what, dtype, shape=None):
+    """Check a contiguous [T, top] array of slots (where it is: _stream)."""
+    if t.dim() != 2 or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous 2-D {dtype} CUDA tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}")
+
+
+def route(logits, top, router=Router()):
+    """The `top` experts of every token and their weights from the logits
+    [T, E], bf16 or float32 (see mx_route): (ids int32 [T, top], weights
+    float32 [T, top])."""
+    lib = load_library()
+    ld = _check_rows(logits, "route: logits")
+    st = _stream(logits)
+    T, E = logits.shape
+    ids = logits.new_empty((T, top), dtype=torch.int32)
+    weights = logits.new_empty((T, top), dtype=torch.float32)
+    cfg = router.c_struct()
+    _check(lib.mx_route(_ptr(logits), _DTYPE[logits.dtype], T, E, ld, top, ctypes.byref(cfg), _ptr(ids),
+                        _ptr(weights), st))
+    return ids, weights
+
+
+def route_backward(dweights, logits, ids, router=Router(), out=None):
+    """The gradient [T, E] of route's weights by the logits for the gradient
+    dweights [T, top] and the choice ids (see mx_route_backward)."""
+    lib = load_library()
+    ld = _check_rows(logits, "route_backward: logits")
+    T, E = logits.shape
+    _slots(ids, "route_backward: ids", torch.int32)
+    _slots(dweights, "route_backward: dweights", torch.float32, ids.shape)
+    if ids.shape[0] != T:
+        raise ValueError(f"route_backward: ids must have {T} rows")
+    st = _stream(logits, dweights, ids, out)
+    if out is None:
+        out, ldo = logits.new_empty((T, E)), E
+    else:
+        ldo = _check_rows(out, "route_backward: out", (T, E), logits.dtype)
+    cfg = router.c_struct()
+    _check(lib.mx_route_backward(_ptr(dweights), _ptr(logits), _DTYPE[logits.dtype], T, E, ld, _ptr(ids),
+                                 ids.shape[1], ctypes.byref(cfg), _ptr(out), ldo, st))
+    return out
+
+
+def expert_sort(ids, E):
+    """The slots (token, choice) of ids [T, top] int32 sorted by expert (see
+    mx_expert_sort): (offsets [E+1], rows [T*top], dest [T, top]), int32.
+    offsets is what the grouped products take, rows what quantize_gather does
+    and dest what quantize_scatter, expert_dispatch and expert_combine do; a
+    slot whose id is outside [0, E) is dropped (dest -1)."""
+    lib = load_library()
+    _slots(ids, "expert_sort: ids", torch.int32)
+    st = _stream(ids)
+    T, top = ids.shape
+    # (E may be refused: the library answers before it looks at the buffers)
+    offsets, rows, dest = ids.new_empty(max(E, 0) + 1), ids.new_empty(T * top), ids.new_empty((T, top))
+    nbytes = lib.mx_expert_sort_workspace_size(T, top, E)
+    ws = ids.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+    _check(lib.mx_expert_sort(_ptr(ids), T, top, E, _ptr(offsets), _ptr(rows), _ptr(dest), _ptr(ws), nbytes, st))
+    return offsets, rows, dest
+
+
+def expert_dispatch(x, dest, rows_out=None, out=None):
+    """Rows x[t] of a 2-D bf16/float32 CUDA tensor copied to their sorted rows
+    dest[t, j] (see mx_expert_dispatch); out (or a new [rows_out, C] tensor, by
+    default a row per slot) receives them.  Rows that dest does not name are not
+    written.  The gradient is expert_combine without weights."""
+    lib = load_library()
+    ldx = _check_rows(x, "expert_dispatch: x")
+    T, C = x.shape
+    _slots(dest, "expert_dispatch: dest", torch.int32)
+    if dest.shape[0] != T:
+        raise ValueError(f"expert_dispatch: dest must have {T} rows")
+    st = _stream(x, dest, out)
+    if out is None:
+        rows_out = dest.numel() if rows_out is None else rows_out
+        out, ldo = x.new_empty((rows_out, C)), C
+    else:
+        ldo = _check_rows(out, "expert_dispatch: out", (out.shape[0] if rows_out is None else rows_out, C), x.dtype)
+    _check(lib.mx_expert_dispatch(_ptr(x), _DTYPE[x.dtype], T, C, ldx, _ptr(dest), dest.shape[1], _ptr(out),
+                                  out.shape[0], ldo, st))
+    return out
+
+
+def expert_combine(y, dest, weights=None, residual=None, out=None):
+    """The expert rows y [rows, C] back to their tokens (see mx_expert_combine):
+    out[t] = sum_j weights[t, j] * y[dest[t, j]] + residual[t], weights float32
+    [T, top] (None: 1).  Dropped slots add nothing; out may be residual."""
+    lib = load_library()
+    ldy = _check_rows(y, "expert_combine: y")
+    rows, C = y.shape
+    _slots(dest, "expert_combine: dest", torch.int32)
+    T, top = dest.shape
+    if weights is not None:
+        _slots(weights, "expert_combine: weights", torch.float32, dest.shape)
+    ldr = 0
+    if residual is not None:
+        ldr = _check_rows(residual, "expert_combine: residual", (T, C), y.dtype)
+    st = _stream(y, dest, weights, residual, out)
+    if out is None:
+        out, ldo = y.new_empty((T, C)), C
+    else:
+        ldo = _check_rows(out, "expert_combine: out", (T, C), y.dtype)
+    _check(lib.mx_expert_combine(_ptr(y), _DTYPE[y.dtype], rows, C, ldy, _ptr(dest), _ptr(weights), T, top,
+                                 _ptr(residual), ldr, _ptr(out), ldo, st))
+    return out
+
+
+def expert_combine_backward(dout, y, dest, weights, out=None):
+    """The gradients (dy, dweights) of expert_combine for the gradient dout
+    [T, C] (see mx_expert_combine_backward); out receives dy [rows, C], whose
+    rows that dest does not name are not written."""
+    lib = load_library()
+    ldy = _check_rows(y, "expert_combine_backward: y")
+    rows, C = y.shape
+    _slots(dest, "expert_combine_backward: dest", torch.int32)
+    _slots(weights, "expert_combine_backward: weights", torch.float32, dest.shape)
+    T, top = dest.shape
+    lddo = _check_rows(dout, "expert_combine_backward: dout", (T, C), y.dtype)
+    st = _stream(y, dout, dest, weights, out)
+    if out is None:
+        out, ldo = y.new_empty((rows, C)), C
+    else:
+        ldo = _check_rows(out, "expert_combine_backward: out", (rows, C), y.dtype)
+    dweights = weights.new_empty((T, top))
+    _check(lib.mx_expert_combine_backward(_ptr(dout), _DTYPE[y.dtype], T, C, lddo, _ptr(y), rows, ldy, _ptr(dest),
+                                          _ptr(weights), top, _ptr(out), ldo, _ptr(dweights), st))
+    return out, dweights
+
+
+def bias_grad(dp, offsets=None, dtype=torch.float32):
+    """The sums of the columns of dp [M, N], the gradient of a bias [N]; with
+    offsets [E+1] those of each expert's rows, [E, N] (see mx_bias_grad and
+    mx_grouped_bias_grad)."""
+    lib = load_library()
+    ld = _check_rows(dp, "bias_grad: dp")
+    if dtype not in _DTYPE:
+        raise ValueError("bias_grad: dtype must be bf16 or float32")
+    M, N = dp.shape
+    if offsets is None:
+        st = _stream(dp)
+        E, group, shape, f = 1, (), (N,), lib.mx_bias_grad
+    else:
+        E = offsets.numel() - 1
+        _check_offsets(offsets, E)
+        if E < 1:
+            raise ValueError("bias_grad: offsets must have at least two entries")
+        st = _stream(dp, offsets)
+        group, shape, f = (_ptr(offsets), E), (E, N), lib.mx_grouped_bias_grad
+    out = dp.new_empty(shape, dtype=dtype)
+    nbytes = lib.mx_bias_grad_workspace_size(M, N, E)
+    ws = dp.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+    _check(f(_ptr(dp), _DTYPE[dp.dtype], M, N, ld, *group, _ptr(out), _DTYPE[dtype], _ptr(ws), nbytes, st))
     return out
 
 

@@ -15,6 +15,7 @@
 //    operands staged through a ring in LDS; a wave's two B tiles are its
 //    columns' gates and ups.
 #include "gate_device.h"
+#include "group_device.h"
 #include "mx_device.h"
 #include "mx_launch.h"
 
@@ -30,48 +31,6 @@ template <int F>
 constexpr int mfma_fmt() {
   if constexpr (F == 0) return 4;
   else return ElemT<F>::MFMA;
-}
-
-// The expert and rows of row tile `slot` (TM rows each, numbered in expert
-// order) from the device offsets, clamped to [0, cap]; every wave works it out
-// by itself.  False past the last tile.
-template <int TM>
-__device__ __forceinline__ bool find_slot(const int32_t* __restrict__ off, int E, int64_t cap, int64_t slot, int& ex,
-                                          int64_t& row0, int& rows) {
-  const int lane = threadIdx.x & 63;
-  int64_t carry = 0;
-  for (int base = 0; base < E; base += 64) {
-    const int e = base + lane;
-    int64_t l0 = 0, h0 = 0;
-    if (e < E) {
-      l0 = off[e];
-      h0 = off[e + 1];
-      l0 = l0 < 0 ? 0 : (l0 > cap ? cap : l0);
-      h0 = h0 < l0 ? l0 : (h0 > cap ? cap : h0);
-    }
-    const int tiles = (int)((h0 - l0 + TM - 1) / TM);
-    int incl = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += v;
-    }
-    const int64_t s = slot - carry;
-    const unsigned long long m = __ballot(s >= incl - tiles && s < incl);
-    if (m) {
-      const int src = __ffsll((long long)m) - 1;
-      const int pre = __shfl(incl - tiles, src, 64);
-      const int lo = __shfl((int)l0, src, 64), hi = __shfl((int)h0, src, 64);
-      ex = __builtin_amdgcn_readfirstlane(base + src);
-      const int r = __builtin_amdgcn_readfirstlane(lo + (int)(s - pre) * TM);
-      const int n = __builtin_amdgcn_readfirstlane(hi) - r;
-      row0 = r;
-      rows = n < TM ? n : TM;
-      return true;
-    }
-    carry += __shfl(incl, 63, 64);
-  }
-  return false;
 }
 
 // One operand row as a lane sees it.

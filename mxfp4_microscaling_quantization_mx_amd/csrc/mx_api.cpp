@@ -919,4 +919,271 @@ mx_status mx_dropout(const void* x, int32_t dtype, int64_t R, int64_t C, int64_t
   return hip_status(mx::launch_dropout(a, static_cast<hipStream_t>(stream)), what);
 }
 
+// ---------------------------------------------------------------- expert layer
+namespace {
+
+constexpr int32_t EXPERTS_MAX = 1024, CHOICES_MAX = 64;
+
+mx_status router_args(const void* logits, int32_t dtype, int64_t T, int32_t E, int64_t ld, int32_t top,
+                      const mx_router_cfg* cfg, const char* what, mx::RouteArgs& a) {
+  if (!known_dtype(dtype)) return fail(MX_ERR_INVALID_ARG, "%s: unknown dtype %d", what, dtype);
+  if (!cfg) return fail(MX_ERR_INVALID_ARG, "%s: null router configuration", what);
+  if (cfg->score != MX_SCORE_SOFTMAX && cfg->score != MX_SCORE_SIGMOID)
+    return fail(MX_ERR_INVALID_ARG, "%s: unknown score %d", what, cfg->score);
+  if (cfg->renormalize != 0 && cfg->renormalize != 1)
+    return fail(MX_ERR_INVALID_ARG, "%s: renormalize must be 0 or 1", what);
+  if (!std::isfinite(cfg->scale)) return fail(MX_ERR_INVALID_ARG, "%s: scale must be finite", what);
+  if (T < 0) return fail(MX_ERR_INVALID_ARG, "%s: negative shape", what);
+  if (E < 1) return fail(MX_ERR_INVALID_ARG, "%s: E=%d < 1", what, E);
+  if (top < 1 || top > E) return fail(MX_ERR_INVALID_ARG, "%s: top=%d is not in 1 .. E=%d", what, top, E);
+  if (E > EXPERTS_MAX || top > CHOICES_MAX || T > 0x7FFFFFFF)
+    return fail(MX_ERR_UNSUPPORTED, "%s: at most %d experts, %d choices and 2^31 - 1 tokens", what, EXPERTS_MAX,
+                CHOICES_MAX);
+  if (T == 0) return MX_OK;
+  mx_status st = check_rows(logits, dtype, E, ld, what, "logits");
+  if (st != MX_OK) return st;
+  a = mx::RouteArgs{};
+  a.logits = logits;
+  a.T = T;
+  a.ld = ld;
+  a.E = E;
+  a.top = top;
+  a.bf16 = dtype == MX_DT_BF16;
+  a.sigmoid = cfg->score == MX_SCORE_SIGMOID;
+  a.renorm = cfg->renormalize == 1;
+  a.scale = cfg->scale;
+  return MX_OK;
+}
+
+mx_status check_words(const void* p, const char* what, const char* name) {
+  if (!p || !aligned(p, 4)) return fail(MX_ERR_INVALID_ARG, "%s: null or unaligned %s", what, name);
+  return MX_OK;
+}
+
+// The shape of a dispatch or combine: T tokens of `top` choices, `rows` sorted
+// rows, C columns.
+mx_status combine_args(int32_t dtype, int64_t T, int64_t C, int64_t rows, int32_t top, const int32_t* dest,
+                       const char* what, mx::CombineArgs& a) {
+  if (!known_dtype(dtype)) return fail(MX_ERR_INVALID_ARG, "%s: unknown dtype %d", what, dtype);
+  if (T < 0 || C < 0 || rows < 0) return fail(MX_ERR_INVALID_ARG, "%s: negative shape", what);
+  if (top < 1) return fail(MX_ERR_INVALID_ARG, "%s: top=%d < 1", what, top);
+  // (a wave per row at least; 64 pieces of 4 elements per wave)
+  if (T > 0x7FFFFFFF || C > 0x7FFFFFFF || T * ((C + 255) / 256) > 0x7FFFFFFF)
+    return fail(MX_ERR_UNSUPPORTED, "%s: too many rows or columns", what);
+  if (T && C) {
+    mx_status st = check_words(dest, what, "dest");
+    if (st != MX_OK) return st;
+  }
+  a = mx::CombineArgs{};
+  a.T = T;
+  a.C = C;
+  a.rows = rows;
+  a.top = top;
+  a.bf16 = dtype == MX_DT_BF16;
+  a.dest = dest;
+  return MX_OK;
+}
+
+}  // namespace
+
+mx_status mx_route(const void* logits, int32_t dtype, int64_t T, int32_t E, int64_t ld, int32_t top,
+                   const mx_router_cfg* cfg, int32_t* ids, float* weights, void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_route";
+  mx::RouteArgs a;
+  mx_status st = router_args(logits, dtype, T, E, ld, top, cfg, what, a);
+  if (st != MX_OK || T == 0) return st;
+  st = check_words(ids, what, "ids");
+  if (st == MX_OK) st = check_words(weights, what, "weights");
+  if (st != MX_OK) return st;
+  a.ids = ids;
+  a.weights = weights;
+  return hip_status(mx::launch_route(a, static_cast<hipStream_t>(stream)), what);
+}
+
+mx_status mx_route_backward(const float* dweights, const void* logits, int32_t dtype, int64_t T, int32_t E, int64_t ld,
+                            const int32_t* ids, int32_t top, const mx_router_cfg* cfg, void* dlogits, int64_t ldd,
+                            void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_route_backward";
+  mx::RouteArgs a;
+  mx_status st = router_args(logits, dtype, T, E, ld, top, cfg, what, a);
+  if (st != MX_OK || T == 0) return st;
+  st = check_words(ids, what, "ids");
+  if (st == MX_OK) st = check_words(dweights, what, "dweights");
+  if (st == MX_OK) st = check_rows(dlogits, dtype, E, ldd, what, "dlogits");
+  if (st != MX_OK) return st;
+  a.ids = const_cast<int32_t*>(ids);
+  a.dweights = dweights;
+  a.dlogits = dlogits;
+  a.ldd = ldd;
+  return hip_status(mx::launch_route(a, static_cast<hipStream_t>(stream)), what);
+}
+
+size_t mx_expert_sort_workspace_size(int64_t T, int32_t top, int32_t E) {
+  if (T <= 0 || top < 1 || E < 1 || E > EXPERTS_MAX || T > 0x7FFFFFFF / top) return 0;
+  return mx::sort_workspace(T * top, E);
+}
+
+mx_status mx_expert_sort(const int32_t* ids, int64_t T, int32_t top, int32_t E, int32_t* offsets, int32_t* rows,
+                         int32_t* dest, void* workspace, size_t ws_bytes, void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_expert_sort";
+  if (T < 0) return fail(MX_ERR_INVALID_ARG, "%s: negative shape", what);
+  if (top < 1) return fail(MX_ERR_INVALID_ARG, "%s: top=%d < 1", what, top);
+  if (E < 1) return fail(MX_ERR_INVALID_ARG, "%s: E=%d < 1", what, E);
+  if (E > EXPERTS_MAX || T > 0x7FFFFFFF / top)
+    return fail(MX_ERR_UNSUPPORTED, "%s: at most %d experts and 2^31 - 1 slots", what, EXPERTS_MAX);
+  mx_status st = check_words(offsets, what, "offsets");
+  if (st == MX_OK && T) st = check_words(ids, what, "ids");
+  if (st == MX_OK && T) st = check_words(rows, what, "rows");
+  if (st == MX_OK && T) st = check_words(dest, what, "dest");
+  if (st != MX_OK) return st;
+  const size_t need = mx::sort_workspace(T * top, E);
+  if (need && (!workspace || ws_bytes < need || !aligned(workspace, 4)))
+    return fail(MX_ERR_INVALID_ARG, "%s: needs a 4-byte aligned workspace of %zu bytes (got %zu bytes at %p)", what,
+                need, ws_bytes, workspace);
+  mx::SortArgs a{};
+  a.ids = ids;
+  a.n = T * top;
+  a.top = top;
+  a.E = E;
+  a.offsets = offsets;
+  a.rows = rows;
+  a.dest = dest;
+  a.ws = static_cast<int*>(workspace);
+  return hip_status(mx::launch_expert_sort(a, static_cast<hipStream_t>(stream)), what);
+}
+
+mx_status mx_expert_dispatch(const void* x, int32_t dtype, int64_t T, int64_t C, int64_t ldx, const int32_t* dest,
+                             int32_t top, void* xs, int64_t rows, int64_t ldxs, void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_expert_dispatch";
+  mx::CombineArgs a;
+  mx_status st = combine_args(dtype, T, C, rows, top, dest, what, a);
+  if (st != MX_OK || T == 0 || C == 0 || rows == 0) return st;
+  st = check_rows(x, dtype, C, ldx, what, "x");
+  if (st == MX_OK) st = check_rows(xs, dtype, C, ldxs, what, "xs");
+  if (st != MX_OK) return st;
+  a.dout = x;
+  a.lddo = ldx;
+  a.dy = xs;
+  a.lddy = ldxs;
+  return hip_status(mx::launch_dispatch(a, static_cast<hipStream_t>(stream)), what);
+}
+
+mx_status mx_expert_combine(const void* y, int32_t dtype, int64_t rows, int64_t C, int64_t ldy, const int32_t* dest,
+                            const float* weights, int64_t T, int32_t top, const void* residual, int64_t ldr, void* out,
+                            int64_t ldo, void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_expert_combine";
+  mx::CombineArgs a;
+  mx_status st = combine_args(dtype, T, C, rows, top, dest, what, a);
+  if (st != MX_OK || T == 0 || C == 0) return st;
+  if (!aligned(weights, 4)) return fail(MX_ERR_INVALID_ARG, "%s: unaligned weights", what);
+  if (rows) st = check_rows(y, dtype, C, ldy, what, "y");
+  if (st == MX_OK && residual) st = check_rows(residual, dtype, C, ldr, what, "residual");
+  if (st == MX_OK) st = check_rows(out, dtype, C, ldo, what, "out");
+  if (st != MX_OK) return st;
+  a.weights = weights;
+  a.y = y;
+  a.ldy = ldy;
+  a.residual = residual;
+  a.ldr = ldr;
+  a.out = out;
+  a.ldo = ldo;
+  if (rows == 0) a.top = 0;                  // no row to take: zeros, or the residual
+  return hip_status(mx::launch_combine(a, static_cast<hipStream_t>(stream)), what);
+}
+
+mx_status mx_expert_combine_backward(const void* dout, int32_t dtype, int64_t T, int64_t C, int64_t lddo,
+                                     const void* y, int64_t rows, int64_t ldy, const int32_t* dest,
+                                     const float* weights, int32_t top, void* dy, int64_t lddy, float* dweights,
+                                     void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_expert_combine_backward";
+  mx::CombineArgs a;
+  mx_status st = combine_args(dtype, T, C, rows, top, dest, what, a);
+  if (st != MX_OK || T == 0) return st;
+  // (without rows or columns every dweight is still a sum, of nothing)
+  st = check_words(dest, what, "dest");
+  if (st == MX_OK) st = check_words(weights, what, "weights");
+  if (st == MX_OK) st = check_words(dweights, what, "dweights");
+  if (st == MX_OK && C && rows) st = check_rows(dout, dtype, C, lddo, what, "dout");
+  if (st == MX_OK && C && rows) st = check_rows(y, dtype, C, ldy, what, "y");
+  if (st == MX_OK && C && rows) st = check_rows(dy, dtype, C, lddy, what, "dy");
+  if (st != MX_OK) return st;
+  if (rows == 0) a.C = 0;                    // nothing may be read
+  a.dout = dout;
+  a.lddo = lddo;
+  a.y = y;
+  a.ldy = ldy;
+  a.weights = weights;
+  a.dy = dy;
+  a.lddy = lddy;
+  a.dweights = dweights;
+  return hip_status(mx::launch_combine_backward(a, static_cast<hipStream_t>(stream)), what);
+}
+
+namespace {
+
+mx_status bias_grad(const void* dp, int32_t dtype, int64_t M, int64_t N, int64_t ld, bool grouped,
+                    const int32_t* offsets, int32_t E, void* out, int32_t out_dtype, void* workspace, size_t ws_bytes,
+                    void* stream, const char* what) {
+  if (!known_dtype(dtype)) return fail(MX_ERR_INVALID_ARG, "%s: unknown dtype %d", what, dtype);
+  if (!known_dtype(out_dtype)) return fail(MX_ERR_INVALID_ARG, "%s: unknown output dtype %d", what, out_dtype);
+  if (M < 0 || N < 0) return fail(MX_ERR_INVALID_ARG, "%s: negative shape", what);
+  if (E < 1) return fail(MX_ERR_INVALID_ARG, "%s: E=%d < 1", what, E);
+  if (grouped) {
+    mx_status st = check_words(offsets, what, "group offsets");
+    if (st != MX_OK) return st;
+  }
+  if (N == 0) return MX_OK;
+  if (M > 0x7FFFFFFF || N > 0x7FFFFFFF || !mx::bias_grad_fits(M, N, E, grouped))
+    return fail(MX_ERR_UNSUPPORTED, "%s: too many rows or columns", what);
+  if (!out || !aligned(out, dtype_size(out_dtype)))
+    return fail(MX_ERR_INVALID_ARG, "%s: null out, or not aligned to its element size", what);
+  if (M) {
+    mx_status st = check_rows(dp, dtype, N, ld, what, "dp");
+    if (st != MX_OK) return st;
+  }
+  const size_t need = mx::bias_grad_workspace(M, N, E, grouped);
+  if (need && (!workspace || ws_bytes < need || !aligned(workspace, 4)))
+    return fail(MX_ERR_INVALID_ARG, "%s: needs a 4-byte aligned workspace of %zu bytes (got %zu bytes at %p)", what,
+                need, ws_bytes, workspace);
+  mx::BiasGradArgs a{};
+  a.dp = dp;
+  a.M = M;
+  a.N = N;
+  a.ld = ld;
+  a.bf16 = dtype == MX_DT_BF16;
+  a.offsets = offsets;
+  a.E = E;
+  a.out = out;
+  a.out_bf16 = out_dtype == MX_DT_BF16;
+  a.ws = static_cast<float*>(workspace);
+  return hip_status(mx::launch_bias_grad(a, static_cast<hipStream_t>(stream)), what);
+}
+
+}  // namespace
+
+size_t mx_bias_grad_workspace_size(int64_t M, int64_t N, int32_t E) {
+  if (M <= 0 || N <= 0 || E < 1 || M > 0x7FFFFFFF || N > 0x7FFFFFFF) return 0;
+  return mx::bias_grad_workspace(M, N, E, true);     // (a grouped call's, no less than a dense one's)
+}
+
+mx_status mx_bias_grad(const void* dp, int32_t dtype, int64_t M, int64_t N, int64_t ld, void* out, int32_t out_dtype,
+                       void* workspace, size_t ws_bytes, void* stream) {
+  g_err[0] = '\0';
+  return bias_grad(dp, dtype, M, N, ld, false, nullptr, 1, out, out_dtype, workspace, ws_bytes, stream, "mx_bias_grad");
+}
+
+mx_status mx_grouped_bias_grad(const void* dp, int32_t dtype, int64_t M, int64_t N, int64_t ld,
+                               const int32_t* d_group_offsets, int32_t E, void* out, int32_t out_dtype, void* workspace,
+                               size_t ws_bytes, void* stream) {
+  g_err[0] = '\0';
+  return bias_grad(dp, dtype, M, N, ld, true, d_group_offsets, E, out, out_dtype, workspace, ws_bytes, stream,
+                   "mx_grouped_bias_grad");
+}
+
 }  // extern "C"

@@ -32,6 +32,40 @@ __device__ __forceinline__ uint32_t quad_xor2(uint32_t v) {
 __device__ __forceinline__ float quad_xor1f(float v) { return __uint_as_float(quad_xor1(__float_as_uint(v))); }
 __device__ __forceinline__ float quad_xor2f(float v) { return __uint_as_float(quad_xor2(__float_as_uint(v))); }
 
+// Reductions over aligned groups of G lanes (a power of two), the result in every
+// lane: neighbours and quads by DPP, 16-lane rows by mirrors, then the gfx950 row
+// and half-wave swaps.  Every lane of the wave must be active.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+template <int G, class Op>
+__device__ __forceinline__ uint32_t group_reduce(uint32_t v, Op op) {
+  if constexpr (G > 1) v = op(v, dpp<0xB1>(v));    // lane ^ 1
+  if constexpr (G > 2) v = op(v, dpp<0x4E>(v));    // lane ^ 2
+  if constexpr (G > 4) v = op(v, dpp<0x141>(v));   // the other quad of 8 lanes (half-row mirror)
+  if constexpr (G > 8) v = op(v, dpp<0x140>(v));   // the other half of 16 lanes (row mirror)
+  if constexpr (G > 16) {
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = op(a[0], a[1]);
+  }
+  if constexpr (G > 32) {
+    const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = op(a[0], a[1]);
+  }
+  return v;
+}
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+  return __uint_as_float(group_reduce<G>(__float_as_uint(v), [](uint32_t x, uint32_t y) {
+    return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
+  }));
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  return group_reduce<G>(v, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+}
+
 // ---------------------------------------------------------------- Philox4x32-10
 // Salmon et al., SC'11: ten rounds of two 32x32->64 multiplies, key bumped by
 // the Weyl constants between rounds.

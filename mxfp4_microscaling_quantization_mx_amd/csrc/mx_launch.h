@@ -231,6 +231,77 @@ struct GatedArgs {
   int64_t stride_codes = 0, stride_scales = 0;
 };
 
+// ---------------------------------------------------------------- expert layer
+// The router (ids and weights out), or with dlogits its backward pass (ids and
+// dweights in).
+struct RouteArgs {
+  const void* logits;
+  int64_t T, ld;
+  int32_t E, top;
+  bool bf16;                  // logits and dlogits (else float32)
+  bool sigmoid, renorm;
+  float scale;
+  int32_t* ids;               // [T, top]
+  float* weights;             // [T, top]
+  const float* dweights = nullptr;
+  void* dlogits = nullptr;
+  int64_t ldd = 0;
+  bool vec = false;           // rows can be read a lane's logits at a time (set by the launch)
+};
+hipError_t launch_route(const RouteArgs& a, hipStream_t st);
+
+struct SortArgs {
+  const int32_t* ids;         // n = T * top slots
+  int64_t n;
+  int32_t top, E;
+  int32_t* offsets;           // [E + 1]
+  int32_t* rows;              // [n]
+  int32_t* dest;              // [n]
+  int* ws;                    // sort_workspace bytes
+  int64_t chunks = 0;         // set by the launch, with the bits of an expert's number
+  int bits = 0;
+};
+size_t sort_workspace(int64_t n, int32_t E);
+hipError_t launch_expert_sort(const SortArgs& a, hipStream_t st);
+
+// Combine, its backward pass and the dispatch (x in dout, xs in dy).
+struct CombineArgs {
+  int64_t T, C, rows;         // rows: of y, dy
+  int32_t top;
+  bool bf16;
+  const int32_t* dest;        // [T, top]
+  const float* weights;       // [T, top], nullable in combine
+  const void* y;
+  int64_t ldy;
+  const void* residual;       // nullable
+  int64_t ldr;
+  void* out;
+  int64_t ldo;
+  const void* dout;
+  int64_t lddo;
+  void* dy;
+  int64_t lddy;
+  float* dweights;
+};
+hipError_t launch_combine(const CombineArgs& a, hipStream_t st);
+hipError_t launch_dispatch(const CombineArgs& a, hipStream_t st);
+hipError_t launch_combine_backward(const CombineArgs& a, hipStream_t st);
+
+// Column sums [E, N] of dp [M, N]: dense (offsets null, E = 1) or per expert.
+struct BiasGradArgs {
+  const void* dp;
+  int64_t M, N, ld;
+  bool bf16;
+  const int32_t* offsets;     // nullable
+  int32_t E;
+  void* out;
+  bool out_bf16;
+  float* ws;                  // bias_grad_workspace bytes
+};
+size_t bias_grad_workspace(int64_t M, int64_t N, int32_t E, bool grouped);
+bool bias_grad_fits(int64_t M, int64_t N, int32_t E, bool grouped);
+hipError_t launch_bias_grad(const BiasGradArgs& a, hipStream_t st);
+
 hipError_t launch_layer_norm(const NormArgs& a, hipStream_t st);
 size_t norm_backward_workspace(int64_t R, int64_t C);
 hipError_t launch_layer_norm_backward(const NormBwdArgs& a, hipStream_t st);

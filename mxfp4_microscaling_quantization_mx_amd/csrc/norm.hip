@@ -57,26 +57,8 @@ __device__ __forceinline__ float ldw(const void* p, bool bf16, int64_t i) {
   return bf16 ? ld1<true>(p, i) : ld1<false>(p, i);
 }
 
-// Sum of v over the 64 lanes, in every lane: neighbours and quads by DPP, the
-// 16-lane rows by mirrors, then the gfx950 row and half-wave swaps.
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
-}
-__device__ __forceinline__ float wave_sum(float v) {
-#define MX_DPP_ADD(CTRL) v = v + __uint_as_float(dpp<CTRL>(__float_as_uint(v)))
-  MX_DPP_ADD(0xB1);    // lane ^ 1
-  MX_DPP_ADD(0x4E);    // lane ^ 2
-  MX_DPP_ADD(0x141);   // the other quad of 8 lanes (half-row mirror)
-  MX_DPP_ADD(0x140);   // the other half of 16 lanes (row mirror)
-#undef MX_DPP_ADD
-  const uint32_t u = __float_as_uint(v);
-  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  const uint32_t t = __float_as_uint(v);
-  const auto b = __builtin_amdgcn_permlane32_swap(t, t, false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
+// Sum of v over the 64 lanes, in every lane.
+__device__ __forceinline__ float wave_sum(float v) { return group_sum<64>(v); }
 __device__ __forceinline__ double from_words(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
