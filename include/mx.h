@@ -474,7 +474,8 @@ mx_status mx_clip_count(const void* src, int32_t src_dtype, int64_t R, int64_t C
 typedef enum {
   MX_ACT_SILU = 0,      /* g * sigmoid(alpha g)                                               */
   MX_ACT_GELU = 1,      /* g * (1 + erf(g / sqrt 2)) / 2                                      */
-  MX_ACT_GELU_TANH = 2  /* g * (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2                  */
+  MX_ACT_GELU_TANH = 2, /* g * (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2                  */
+  MX_ACT_NONE = 3       /* g (mx_linear only)                                                 */
 } mx_act;
 
 /* Where the gate and up rows of the weight operand [2N, K] are (and, in the
@@ -753,6 +754,65 @@ mx_status mx_expert_combine_backward(const void* dout, int32_t dtype, int64_t T,
                                      const void* y, int64_t rows, int64_t ldy, const int32_t* dest,
                                      const float* weights, int32_t top, void* dy, int64_t lddy, float* dweights,
                                      void* stream);
+
+/* The epilogue of a linear layer. */
+typedef struct {
+  int32_t act;       /* mx_act                                                     */
+  float alpha;       /* slope of the SiLU's sigmoid (finite, > 0); the others ignore it */
+} mx_epilogue_cfg;
+
+/*
+ * mx_linear — a linear layer on MX operands with its bias, activation and residual in
+ * the product's epilogue, so that the product never reaches memory:
+ *   Y[m, n] = act(P[m, n] + bias[n]) + residual[m, n],   P = A B^T (float32, as mx_gemm).
+ * The formula is evaluated in float32 and rounded once to y_dtype; the activations
+ * err as stated at mx_gemm_gated, the sum of products likewise (no split over
+ * workgroups, no workspace).
+ *
+ *   A, B      host structs of device buffers, as mx_gemm: any element types, 1-D or
+ *             2-D scales; A [M, K], B [N, K].
+ *   cfg       host; NULL = no activation.
+ *   bias      device; [N] of bias_dtype (element-aligned); NULL = none.
+ *   residual  device; [M, N] of r_dtype, row stride ldr (>= N); NULL = none.
+ *   Y         device; [M, N] of y_dtype, row stride ldy (>= N).  May be residual itself
+ *             (the same type, base and stride).
+ *   M or N = 0: nothing is written.  K = 0: the product is zero.
+ */
+mx_status mx_linear(const mx_tensor* A, const mx_tensor* B, const mx_epilogue_cfg* cfg, const void* bias,
+                    int32_t bias_dtype, const void* residual, int32_t r_dtype, int64_t ldr, void* Y, int32_t y_dtype,
+                    int64_t ldy, void* stream);
+
+/*
+ * mx_linear_backward — the gradient of mx_linear through its activation,
+ *   dP[m, n] = dY[m, n] * act'(P[m, n] + bias[n]),
+ * with the product recomputed from A and B in the same kernel (nothing is saved by
+ * the forward pass).  The data and weight gradients are products of dP like any
+ * linear layer's (mx_quantize of dP, mx_gemm), the bias's is mx_bias_grad of dP and
+ * the residual's dY itself.  cfg's act must not be MX_ACT_NONE, whose dP is dY.
+ *
+ *   dY     device; [M, N] of dy_dtype, row stride lddy (>= N).
+ *   dP     device; [M, N] of dp_dtype, row stride lddp (>= N).  May be dY itself (the
+ *          same type, base and stride).
+ */
+mx_status mx_linear_backward(const mx_tensor* A, const mx_tensor* B, const mx_epilogue_cfg* cfg, const void* bias,
+                             int32_t bias_dtype, const void* dY, int32_t dy_dtype, int64_t lddy, void* dP,
+                             int32_t dp_dtype, int64_t lddp, void* stream);
+
+/*
+ * mx_grouped_linear, mx_grouped_linear_backward — the same for rows grouped by expert:
+ * rows [off[e], off[e+1]) of A, residual, Y, dY and dP belong to expert e, whose bias
+ * is at bias + e * bias_stride elements.  Groups, offsets, expert strides and A (1-D
+ * scales) as in mx_grouped_gemm; rows past off[E] are neither read nor written.
+ */
+mx_status mx_grouped_linear(const mx_tensor* A, const int32_t* d_group_offsets, int32_t E, const mx_tensor* B,
+                            int64_t expert_stride_codes, int64_t expert_stride_scales, const mx_epilogue_cfg* cfg,
+                            const void* bias, int32_t bias_dtype, int64_t bias_stride, const void* residual,
+                            int32_t r_dtype, int64_t ldr, void* Y, int32_t y_dtype, int64_t ldy, void* stream);
+mx_status mx_grouped_linear_backward(const mx_tensor* A, const int32_t* d_group_offsets, int32_t E, const mx_tensor* B,
+                                     int64_t expert_stride_codes, int64_t expert_stride_scales,
+                                     const mx_epilogue_cfg* cfg, const void* bias, int32_t bias_dtype,
+                                     int64_t bias_stride, const void* dY, int32_t dy_dtype, int64_t lddy, void* dP,
+                                     int32_t dp_dtype, int64_t lddp, void* stream);
 
 /*
  * mx_bias_grad, mx_grouped_bias_grad — the sums of the columns of dp [M, N], the

@@ -38,6 +38,7 @@ _SCALE = {"floor": 0, "round_up": 1, "prescale_3_4": 2}
 # MX element types: name -> (mx_elem, bits per element)
 _ELEM = {"e2m1": (0, 4), "e4m3": (1, 8), "e5m2": (2, 8), "e2m3": (3, 6), "e3m2": (4, 6)}
 _ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+_EPILOGUE_ACT = {**_ACT, None: 3}
 _SCORE = {"softmax": 0, "sigmoid": 1}
 _GATE_LAYOUT = {"interleaved": 0, "halves": 1}
 _DTYPE = {torch.float32: MX_DT_F32, torch.bfloat16: MX_DT_BF16}
@@ -48,7 +49,8 @@ EXPORTED = ("mx_quantize", "mx_quantize_gather", "mx_quantize_scatter", "mx_dequ
             "mx_grouped_gemm_gated", "mx_grouped_gemm_gated_backward", "mx_layer_norm", "mx_layer_norm_backward",
             "mx_layer_norm_backward_workspace_size", "mx_dropout", "mx_route", "mx_route_backward", "mx_expert_sort",
             "mx_expert_sort_workspace_size", "mx_expert_dispatch", "mx_expert_combine", "mx_expert_combine_backward",
-            "mx_bias_grad", "mx_grouped_bias_grad", "mx_bias_grad_workspace_size",
+            "mx_bias_grad", "mx_grouped_bias_grad", "mx_bias_grad_workspace_size", "mx_linear", "mx_linear_backward",
+            "mx_grouped_linear", "mx_grouped_linear_backward",
             "mx_last_error", "mx_version")
 
 
@@ -69,6 +71,10 @@ class QuantCfgC(ctypes.Structure):
 class GateCfgC(ctypes.Structure):
     _fields_ = [("act", ctypes.c_int32), ("layout", ctypes.c_int32), ("alpha", ctypes.c_float),
                 ("limit", ctypes.c_float), ("up_shift", ctypes.c_float)]
+
+
+class EpilogueCfgC(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int32), ("alpha", ctypes.c_float)]
 
 
 class RouterCfgC(ctypes.Structure):
@@ -140,8 +146,14 @@ def load_library(path=LIB_PATH):
     lib.mx_grouped_bias_grad.argtypes = [P, I32, I64, I64, I64, P, I32, P, I32, P, SZ, P]
     lib.mx_bias_grad_workspace_size.argtypes = [I64, I64, I32]
     lib.mx_bias_grad_workspace_size.restype = SZ
+    epilogue = [ctypes.POINTER(EpilogueCfgC), P, I32]
+    lib.mx_linear.argtypes = [PT, PT, *epilogue, P, I32, I64, P, I32, I64, P]
+    lib.mx_grouped_linear.argtypes = [PT, P, I32, PT, I64, I64, *epilogue, I64, P, I32, I64, P, I32, I64, P]
+    lib.mx_linear_backward.argtypes = lib.mx_linear.argtypes
+    lib.mx_grouped_linear_backward.argtypes = lib.mx_grouped_linear.argtypes
     for f in ("mx_route", "mx_route_backward", "mx_expert_sort", "mx_expert_dispatch", "mx_expert_combine",
-              "mx_expert_combine_backward", "mx_bias_grad", "mx_grouped_bias_grad"):
+              "mx_expert_combine_backward", "mx_bias_grad", "mx_grouped_bias_grad", "mx_linear", "mx_linear_backward",
+              "mx_grouped_linear", "mx_grouped_linear_backward"):
         getattr(lib, f).restype = ctypes.c_int
     lib.mx_last_error.restype = ctypes.c_char_p
     lib.mx_last_error.argtypes = []
@@ -805,6 +817,69 @@ def expert_combine_backward(dout, y, dest, weights, out=None):
     _check(lib.mx_expert_combine_backward(_ptr(dout), _DTYPE[y.dtype], T, C, lddo, _ptr(y), rows, ldy, _ptr(dest),
                                           _ptr(weights), top, _ptr(out), ldo, _ptr(dweights), st))
     return out, dweights
+
+
+def _linear(what, a, b, offsets, bias, act, alpha, r, r_name, out_dtype, out):
+    lib = load_library()
+    st = _stream(a.codes, a.scales, b.codes, b.scales, offsets, bias, r, out)
+    if offsets is not None:
+        E, N = b.codes.shape[0], b.codes.shape[1]
+        _check_offsets(offsets, E)
+        bt = MxTensorC(b.codes.data_ptr(), b.scales.data_ptr(), N, b.K, b.codes.stride(1), b.scales.stride(1),
+                       _BLOCK[b.block], _ELEM[b.elem][0])
+        group = (_ptr(offsets), E, ctypes.byref(bt), b.codes.stride(0), b.scales.stride(0))
+    else:
+        N, bt = b.rows, b.c_struct()
+        group = (ctypes.byref(bt),)
+    epilogue = (None, MX_DT_F32)
+    if bias is not None:
+        if offsets is None:
+            _norm_param(bias, N, None, f"{what}: bias")
+            stride = ()
+        else:
+            stride = (_check_rows(bias, f"{what}: bias", (E, N)),)
+        epilogue = (_ptr(bias), _DTYPE[bias.dtype], *stride)
+    elif offsets is not None:
+        epilogue += (0,)
+    shape = (a.rows, N)
+    ldr, rd = 0, MX_DT_F32
+    if r is not None:
+        ldr, rd = _check_rows(r, f"{what}: {r_name}", shape), _DTYPE[r.dtype]
+    if out is None:
+        out, ldo = a.codes.new_empty(shape, dtype=out_dtype), N
+    else:
+        ldo = _check_rows(out, f"{what}: out", shape)
+    at, cfg = a.c_struct(), EpilogueCfgC(_EPILOGUE_ACT[act], alpha)
+    _check(getattr(lib, what)(ctypes.byref(at), *group, ctypes.byref(cfg), *epilogue, _ptr(r), rd, ldr, _ptr(out),
+                              _DTYPE[out.dtype], ldo, st))
+    return out
+
+
+def linear(a, b, bias=None, act=None, residual=None, alpha=1.0, out_dtype=torch.bfloat16, out=None):
+    """act(A B^T + bias) + residual for MX operands a [M, K] and b [N, K], the
+    bias [N], activation (None, "silu" with slope alpha, "gelu", "gelu_tanh")
+    and residual [M, N] in the product's epilogue (see mx_linear).  bias and
+    residual may be bf16 or float32; out may be residual."""
+    return _linear("mx_linear", a, b, None, bias, act, alpha, residual, "residual", out_dtype, out)
+
+
+def linear_backward(a, b, dy, bias=None, act="gelu", alpha=1.0, out_dtype=torch.bfloat16, out=None):
+    """The gradient dy * act'(A B^T + bias) [M, N] of linear through its
+    activation, the product recomputed from a and b (see mx_linear_backward);
+    the bias's gradient is bias_grad of it."""
+    return _linear("mx_linear_backward", a, b, None, bias, act, alpha, dy, "dy", out_dtype, out)
+
+
+def grouped_linear(a, offsets, b, bias=None, act=None, residual=None, alpha=1.0, out_dtype=torch.bfloat16, out=None):
+    """linear for rows grouped by expert; a, offsets and the stacked b [E, N, K]
+    as in grouped_gemm, bias [E, N] (see mx_grouped_linear).  Rows past
+    offsets[E] of the output are not written."""
+    return _linear("mx_grouped_linear", a, b, offsets, bias, act, alpha, residual, "residual", out_dtype, out)
+
+
+def grouped_linear_backward(a, offsets, b, dy, bias=None, act="gelu", alpha=1.0, out_dtype=torch.bfloat16, out=None):
+    """linear_backward for rows grouped by expert."""
+    return _linear("mx_grouped_linear_backward", a, b, offsets, bias, act, alpha, dy, "dy", out_dtype, out)
 
 
 def bias_grad(dp, offsets=None, dtype=torch.float32):

@@ -27,9 +27,10 @@ CFLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-ffp-contract=off", "-Wall", "-Wno-unused-function",
 ]
-SOURCES = ["mx_api.cpp", "quantize.hip", "dequantize.hip", "transpose.hip", "gemm.hip", "gemm_splitk.hip", "clip.hip",
-           "gated.hip", "gated256.hip", "gated_f8.hip", "norm.hip", "dropout.hip", "experts.hip", "combine.hip",
-           "bias_grad.hip"]
+# (those that take longest to compile first)
+SOURCES = ["gemm.hip", "linear_f8.hip", "linear_f8_backward.hip", "gated_f8.hip", "linear256.hip", "gated256.hip",
+           "linear.hip", "gated.hip", "mx_api.cpp", "quantize.hip", "dequantize.hip", "transpose.hip",
+           "gemm_splitk.hip", "clip.hip", "norm.hip", "dropout.hip", "experts.hip", "combine.hip", "bias_grad.hip"]
 
 
 def _run(cmd):

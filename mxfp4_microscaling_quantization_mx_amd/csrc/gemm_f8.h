@@ -235,14 +235,15 @@ __device__ __forceinline__ void f8_compute(v16f acc[2][4], uint32_t slot, uint32
 // multiplied and its result stored.
 // OUT: 0 float32, 1 bf16, 2 the quantizing epilogue (MXFP4 codes and scale
 // bytes along N into qo, from the swapped-operand accumulators), 3 the gated
-// block's epilogue (go: forward, or with dH backward; `halves` its row order).
+// block's epilogue (go: forward, or with dH backward; `halves` its row order), 4 and 5
+// the linear layer's (lo: forward, backward).
 template <int FA, int FB, int OUT, class Sched>
 __device__ __forceinline__ void run_f8(const Sched& sc, const MxOperand& A, const MxOperand& B, int K, void* C,
                                        int64_t ldc, int a_2d, int b_2d, uint8_t* slots, uint32_t* sws,
                                        const t256::QOut& qo = t256::QOut{}, const t256c::GateOut* go = nullptr,
-                                       int halves = 0) {
+                                       int halves = 0, const t256c::LinearOut* lo = nullptr) {
   constexpr bool OUT_BF16 = OUT == 1;
-  constexpr bool GATED = OUT == 3;
+  constexpr bool GATED = OUT == 3, LINEAR = OUT >= 4;
   static_assert(GATED == (Sched::BMAP != t256c::B_ROWS), "the gated epilogue needs the gated row order");
   constexpr bool SWAP = OUT == 2;
   const int ntiles = sc.count();
@@ -263,7 +264,7 @@ __device__ __forceinline__ void run_f8(const Sched& sc, const MxOperand& A, cons
   const int64_t lds_s = sA ? A.ld_scales : B.ld_scales;
   // Tile j of this workgroup: the lane's load state, and the tile's output
   // origin (row of C, column) and extent.
-  auto setup = [&](int j, F8Lane& L, int64_t& crow0, int& n0, int& mlim, int& nlim) {
+  auto setup = [&](int j, F8Lane& L, int64_t& crow0, int& n0, int& mlim, int& nlim, int& ex) {
     const t256::TileInfo ti = sc.tile(j);
     mlim = ti.M - ti.m0;
     nlim = ti.N - ti.n0;
@@ -297,13 +298,14 @@ __device__ __forceinline__ void run_f8(const Sched& sc, const MxOperand& A, cons
     L.so = sr >= 0 ? (uint32_t)((s2d ? (sr >> 5) : sr) * lds_s) : MX_OOB;
     crow0 = ti.c_row0;
     n0 = ti.n0;
+    if constexpr (LINEAR) ex = ti.ex;
   };
   const int nst = (K + 127) / 128;
   const uint32_t a_slots = (uint32_t)(uintptr_t)(f8::lds_t)slots, a_sws = (uint32_t)(uintptr_t)(f8::lds_t)sws;
   F8Lane L;
   int64_t c0 = 0, c0n = 0;
-  int n0 = 0, mlim = 0, nlim = 0, n0n = 0, mln = 0, nln = 0;
-  if (ntiles > 0) setup(0, L, c0, n0, mlim, nlim);
+  int n0 = 0, mlim = 0, nlim = 0, ex = 0, n0n = 0, mln = 0, nln = 0, exn = 0;
+  if (ntiles > 0) setup(0, L, c0, n0, mlim, nlim, ex);
   if (ntiles > 0 && nst > 0) f8_issue<FA, FB>(L, 0, K, slots, sws, wave);
   int g = 0;                                                  // stages multiplied so far (slot g & 1)
   for (int j = 0; j < ntiles; ++j) {
@@ -323,7 +325,7 @@ __device__ __forceinline__ void run_f8(const Sched& sc, const MxOperand& A, cons
         f8_issue<FA, FB>(L, s + 1, K, slots + nx * f8::SLOT, sws + nx * f8::SWORDS, wave);
       } else if (j + 1 < ntiles) {
         // tile j issues nothing more: its load state becomes tile j + 1's
-        setup(j + 1, L, c0n, n0n, mln, nln);
+        setup(j + 1, L, c0n, n0n, mln, nln, exn);
         f8_issue<FA, FB>(L, 0, K, slots + nx * f8::SLOT, sws + nx * f8::SWORDS, wave);
       }
       f8_compute<FA, FB, SWAP>(acc.t, a_slots + (uint32_t)((g & 1) * f8::SLOT),
@@ -346,16 +348,19 @@ __device__ __forceinline__ void run_f8(const Sched& sc, const MxOperand& A, cons
       } else {
         t256::store_tile_gate<false, t256c::B_INTERLEAVED>(acc, q, c0, n0, mlim, nlim);
       }
+    } else if constexpr (LINEAR) {
+      t256::store_tile_linear<OUT == 5>(acc, t256c::load_gate_out(lo), c0, n0, mlim, nlim, ex);
     } else {
       constexpr int ES = OUT_BF16 ? 2 : 4;
       t256::store_tile<OUT_BF16>(acc, static_cast<uint8_t*>(C) + (c0 * ldc + n0) * ES, (int)ldc, mlim, nlim);
     }
     if (j + 1 < ntiles) {
-      if (nst == 0) setup(j + 1, L, c0n, n0n, mln, nln);
+      if (nst == 0) setup(j + 1, L, c0n, n0n, mln, nln, exn);
       c0 = c0n;
       n0 = n0n;
       mlim = mln;
       nlim = nln;
+      ex = exn;
     }
   }
 }

@@ -64,6 +64,7 @@ struct DenseSchedT {
     ti.M = M;
     ti.N = N;
     ti.c_row0 = ti.m0;
+    ti.ex = 0;
     return ti;
   }
 };
@@ -171,6 +172,7 @@ struct GroupedSchedT {
     ti.M = rows;
     ti.N = P.N;
     ti.c_row0 = row0;
+    ti.ex = ex;
     return ti;
   }
 };
@@ -213,6 +215,14 @@ __device__ __forceinline__ void build_expert_table(const int32_t* __restrict__ o
     if (lane == 0) pre[E] = carry;
   }
   __syncthreads();
+}
+
+// The linear epilogue of a launch.
+inline t256c::LinearOut linear_out(const GatedArgs& a) {
+  return t256c::LinearOut{gate_params(a.act, a.alpha, a.limit, a.up_shift),
+                          (a.out_bf16 ? t256c::LIN_OUT_BF16 : 0) | (a.dh_bf16 ? t256c::LIN_R_BF16 : 0) |
+                              (a.bias_bf16 ? t256c::LIN_BIAS_BF16 : 0),
+                          a.out, a.dH, a.bias, a.bias_stride, (int)a.ldo, (int)a.lddh};
 }
 
 }  // namespace

@@ -79,6 +79,7 @@ struct TileInfo {
   // Schedules that split K (Sched::UNITS) hand out units = a range of stages
   // [k0, k0 + ns) of one tile, k0 even; the others always run whole tiles.
   int k0, ns;
+  int ex;                                  // the tile's expert (the linear epilogue's bias row)
 };
 
 // Row strides (bytes) shared by all tiles of a launch.
@@ -115,9 +116,24 @@ struct alignas(16) GateOut {
 };
 static_assert(sizeof(GateOut) == 64, "four 16-byte LDS reads");
 
-// A wave-uniform GateOut kept in LDS, read with one wait (in scalar registers
-// across the pipeline it would spill).
-__device__ __forceinline__ GateOut load_gate_out(const GateOut* p) {
+// Destination of the linear epilogue: Y = act(X + bias) + r, or (BACKWARD) dP = r *
+// act'(X + bias) with r the gradient dY; act 3 is none, bias and r may be null.
+struct alignas(16) LinearOut {
+  GateP p;                                 // act and alpha
+  int flags;                               // LIN_*
+  void* out;
+  const void* r;
+  const void* bias;                        // row of expert ex at ex * bias_stride elements
+  int64_t bias_stride;
+  int ldo, ldr;
+};
+constexpr int LIN_OUT_BF16 = 1, LIN_R_BF16 = 2, LIN_BIAS_BF16 = 4;
+static_assert(sizeof(LinearOut) == 64, "four 16-byte LDS reads");
+
+// A wave-uniform GateOut (LinearOut) kept in LDS, read with one wait (in scalar
+// registers across the pipeline it would spill).
+template <class Out>
+__device__ __forceinline__ Out load_gate_out(const Out* p) {
   typedef int v4 __attribute__((ext_vector_type(4)));
   v4 q[4];
   const uint32_t a = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
@@ -135,7 +151,7 @@ __device__ __forceinline__ GateOut load_gate_out(const GateOut* p) {
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[4 * i + k] = __builtin_amdgcn_readfirstlane(q[i][k]);
-  return __builtin_bit_cast(GateOut, w);
+  return __builtin_bit_cast(Out, w);
 }
 
 // Tile order: groups of GM M-tiles, each walked N-tile by N-tile, so that a
@@ -574,15 +590,20 @@ template <bool OUT_BF16, class Sched>
 __device__ __forceinline__ void store_unit(Acc& acc, const Sched& sc, int j, void* C, int64_t ldc);
 
 // Output kinds of run_tiles: float32, bf16, the quantizing epilogue
-// (MX_T256_SWAP = 1 only), or the gated block's epilogues (forward, backward;
-// MX_T256_SWAP = 0 and a gated Sched::BMAP).
-constexpr int OUT_F32 = 0, OUT_BF16_ = 1, OUT_MX = 2, OUT_GATE = 3, OUT_GATE_BWD = 4;
+// (MX_T256_SWAP = 1 only), the gated block's epilogues (forward, backward;
+// MX_T256_SWAP = 0 and a gated Sched::BMAP), or the linear layer's (MX_T256_SWAP = 0).
+constexpr int OUT_F32 = 0, OUT_BF16_ = 1, OUT_MX = 2, OUT_GATE = 3, OUT_GATE_BWD = 4, OUT_LINEAR = 5,
+              OUT_LINEAR_BWD = 6;
 
 __device__ __forceinline__ void store_tile_mx(const Acc& acc, const QOut& q, int m0, int n0, int mlim, int nlim);
 
 template <bool BWD, int BMAP>
 __device__ __forceinline__ void store_tile_gate(const Acc& acc, const t256c::GateOut& q, int64_t row0, int n0, int mlim,
                                                 int nlim);
+
+template <bool BWD>
+__device__ __forceinline__ void store_tile_linear(const Acc& acc, const t256c::LinearOut& q, int64_t row0, int n0,
+                                                  int mlim, int nlim, int ex);
 
 // Run this workgroup's tiles: C tile = A[m0:m0+256] * B[n0:n0+256]^T over all
 // K for each tile sc.tile(j), j < sc.count().  The stage sequence g = j * nst
@@ -602,9 +623,11 @@ __device__ __forceinline__ void store_tile_gate(const Acc& acc, const t256c::Gat
 template <bool A2D, bool B2D, int OUT, bool SPLIT, class Sched>
 __device__ __forceinline__ void run_tiles(const Sched& sc, const Strides& sd, int K, void* C, int64_t ldc,
                                           uint8_t* lds, const QOut& qo = QOut{},
-                                          const t256c::GateOut* go = nullptr) {
+                                          const t256c::GateOut* go = nullptr,
+                                          const t256c::LinearOut* lo = nullptr) {
   constexpr int BMAP = Sched::BMAP;
-  static_assert((OUT >= OUT_GATE) == (BMAP != t256c::B_ROWS), "the gated epilogues need the gated row order");
+  constexpr bool GATED = OUT == OUT_GATE || OUT == OUT_GATE_BWD;
+  static_assert(GATED == (BMAP != t256c::B_ROWS), "the gated epilogues need the gated row order");
   static_assert((OUT == OUT_MX) == (MX_T256_SWAP != 0), "the quantizing epilogue needs the swapped operand order");
   constexpr bool UNITS = Sched::UNITS;
   static_assert(!UNITS || OUT != OUT_MX, "units end in the split-K epilogue, which stores float32 or bf16");
@@ -619,7 +642,10 @@ __device__ __forceinline__ void run_tiles(const Sched& sc, const Strides& sd, in
   auto store = [&](const TileInfo& ti) {
     if constexpr (OUT == OUT_MX)
       store_tile_mx(acc, qo, (int)ti.c_row0, ti.n0, ti.M - ti.m0, ti.N - ti.n0);
-    else if constexpr (OUT >= OUT_GATE)
+    else if constexpr (OUT >= OUT_LINEAR)
+      store_tile_linear<OUT == OUT_LINEAR_BWD>(acc, t256c::load_gate_out(lo), ti.c_row0, ti.n0, ti.M - ti.m0,
+                                               ti.N - ti.n0, ti.ex);
+    else if constexpr (GATED)
       store_tile_gate<OUT == OUT_GATE_BWD, BMAP>(acc, t256c::load_gate_out(go), ti.c_row0, ti.n0, ti.M - ti.m0, ti.N - ti.n0);
     else
       store_tile<OUT == OUT_BF16_>(acc, static_cast<uint8_t*>(C) + (ti.c_row0 * ldc + ti.n0) * ES, (int)ldc,
@@ -1308,6 +1334,94 @@ __device__ __forceinline__ void store_tile_gate(const Acc& acc, const t256c::Gat
         }
       }
     }
+  }
+}
+
+// ------------------------------------------------------------ linear epilogue
+// The wave's 128 columns are taken as two pairs of MFMA column tiles, each pair in
+// the gated epilogue's pieces (four rows of two column tiles): a lane's bias values,
+// one per column tile, are loaded first, and r and the output travel in whole lines
+// where their layout allows it, exactly as the gated block's dH and h.
+template <int ACT, bool BWD>
+__device__ __forceinline__ void linear_piece_act(const GateP& p, const Acc& acc, int i, int jp, int r4, const float b[2],
+                                                 const GateTile& r, GateTile& y) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float x = acc.t[i][jp + j][4 * r4 + q] + b[j];
+      float d;
+      if constexpr (ACT == 3) y.t[j][q] = x + r.t[j][q];
+      else if constexpr (BWD) gate_act<ACT, true>(p, x, d), y.t[j][q] = r.t[j][q] * d;
+      else y.t[j][q] = gate_act<ACT, false>(p, x, d) + r.t[j][q];
+    }
+}
+
+template <bool BWD>
+__device__ __forceinline__ void store_tile_linear(const Acc& acc, const t256c::LinearOut& q, int64_t row0, int n0,
+                                                  int mlim, int nlim, int ex) {
+  GatePlace pl = gate_place();                       // (its columns count a wave's 64)
+  {
+    const int wn64 = pl.col & 64;
+    pl.col += wn64;
+    pl.line_col += wn64;
+  }
+  const int rows = mlim < 256 ? mlim : 256, cols = nlim < 256 ? nlim : 256;
+  const int out_bf16 = q.flags & t256c::LIN_OUT_BF16, r_bf16 = q.flags & t256c::LIN_R_BF16;
+  const int bias_bf16 = q.flags & t256c::LIN_BIAS_BF16;
+  const __amdgpu_buffer_rsrc_t ro = block_rsrc(q.out, row0, n0, q.ldo, rows, cols, out_bf16 ? 2 : 4);
+  const __amdgpu_buffer_rsrc_t rr =
+      q.r ? block_rsrc(q.r, row0, n0, q.ldr, rows, cols, r_bf16 ? 2 : 4) : rsrc(q.out, 0);   // (none: reads as zeros)
+  const int eb = bias_bf16 ? 2 : 4;
+  const __amdgpu_buffer_rsrc_t rb =
+      q.bias ? rsrc(static_cast<const uint8_t*>(q.bias) + (ex * q.bias_stride + n0) * eb, (uint32_t)(cols * eb))
+             : rsrc(q.out, 0);
+  const bool lines = out_bf16 && ((q.ldo | cols) & 1) == 0 && ((uintptr_t)q.out & 3) == 0;
+  const bool rlines = r_bf16 && ((q.ldr | cols) & 1) == 0 && ((uintptr_t)q.r & 3) == 0;
+#pragma unroll
+  for (int jp = 0; jp < TJ; jp += 2) {
+    const bool line_in = pl.line_col < cols;
+    const uint32_t voff = line_in ? (uint32_t)((pl.line_row * q.ldo + pl.line_col) * 2) : OOB;
+    const uint32_t roff = line_in ? (uint32_t)((pl.line_row * q.ldr + pl.line_col) * 2) : OOB;
+    float b[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t bo = (uint32_t)((pl.col + 32 * j) * eb);
+      b[j] = bias_bf16 ? __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rb, bo, 0, 0) << 16)
+                       : __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rb, bo, 0, 0));
+    }
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      uint32_t w[2][4];
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        if (q.r && rlines && (r4 & 1) == 0) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            w[k >> 2][k & 3] = __builtin_amdgcn_raw_buffer_load_b32(
+                rr, roff, 2 * (32 * i + 8 * (r4 + (k >> 2)) + (k & 2) + 4 * (k & 1)) * q.ldr, 0);
+        }
+        GateTile r, y;
+        if (!q.r) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r.t[j][k] = 0.0f;
+        } else if (rlines) {
+          unpack_piece(w[r4 & 1], pl.sel, r);
+        } else {
+          load_piece(r, i, r4, pl, cols, q.ldr, r_bf16, rr);
+        }
+        if (q.p.act == 0) linear_piece_act<0, BWD>(q.p, acc, i, jp, r4, b, r, y);
+        else if (q.p.act == 1) linear_piece_act<1, BWD>(q.p, acc, i, jp, r4, b, r, y);
+        else if (BWD || q.p.act == 2) linear_piece_act<2, BWD>(q.p, acc, i, jp, r4, b, r, y);
+        else linear_piece_act<3, BWD>(q.p, acc, i, jp, r4, b, r, y);
+        if (lines) store_piece_lines(y, i, r4, pl, voff, q.ldo, ro);
+        else store_piece(y, i, r4, pl, 1, 0, cols, q.ldo, out_bf16, ro);
+      }
+    }
+    pl.col += 64;
+    pl.line_col += 64;
   }
 }
 #endif

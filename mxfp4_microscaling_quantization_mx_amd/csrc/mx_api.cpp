@@ -1186,4 +1186,124 @@ mx_status mx_grouped_bias_grad(const void* dp, int32_t dtype, int64_t M, int64_t
                    "mx_grouped_bias_grad");
 }
 
+// ---------------------------------------------------------------- linear layer
+namespace {
+
+struct Buffer {
+  const void* p;
+  int32_t dtype;
+  int64_t ld;
+};
+
+// Validate a linear layer's operands, epilogue and buffers and describe them: r is the
+// residual (p null: none) or, backward, dY.
+mx_status linear_args(const mx_tensor* A, const mx_tensor* B, const mx_epilogue_cfg* cfg, const void* bias,
+                      int32_t bias_dtype, int64_t bias_stride, bool backward, const Buffer& r, const Buffer& out,
+                      const char* what, mx::GatedArgs& a) {
+  char name[64];
+  std::snprintf(name, sizeof(name), "%s: A", what);
+  mx_status st = check_tensor(A, name);
+  if (st != MX_OK) return st;
+  std::snprintf(name, sizeof(name), "%s: B", what);
+  st = check_tensor(B, name);
+  if (st != MX_OK) return st;
+  if (A->K != B->K)
+    return fail(MX_ERR_INVALID_ARG, "%s: A.K=%lld != B.K=%lld", what, (long long)A->K, (long long)B->K);
+  const int32_t act = cfg ? cfg->act : (int32_t)MX_ACT_NONE;
+  if (act < MX_ACT_SILU || act > MX_ACT_NONE) return fail(MX_ERR_INVALID_ARG, "%s: unknown activation %d", what, act);
+  if (cfg && (!(cfg->alpha > 0.0f) || !std::isfinite(cfg->alpha)))
+    return fail(MX_ERR_INVALID_ARG, "%s: alpha must be finite and > 0", what);
+  if (backward && act == MX_ACT_NONE)
+    return fail(MX_ERR_INVALID_ARG, "%s: without an activation the gradient is dY itself", what);
+  if (!known_dtype(out.dtype)) return fail(MX_ERR_INVALID_ARG, "%s: unknown output dtype %d", what, out.dtype);
+  if (bias && !known_dtype(bias_dtype))
+    return fail(MX_ERR_INVALID_ARG, "%s: unknown bias dtype %d", what, bias_dtype);
+  if ((r.p || backward) && !known_dtype(r.dtype))
+    return fail(MX_ERR_INVALID_ARG, "%s: unknown %s dtype %d", what, backward ? "dY" : "residual", r.dtype);
+  if (A->rows > 0x7FFFFFFF || B->rows > 0x7FFFFFFF || A->K > 0x7FFFFFFF)
+    return fail(MX_ERR_UNSUPPORTED, "%s: at most 2^31 - 1 rows and K elements", what);
+  a = mx::GatedArgs{};
+  a.A = operand(A);
+  a.B = operand(B);
+  a.a_2d = A->block == MX_BLOCK_2D;
+  a.b_2d = B->block == MX_BLOCK_2D;
+  a.a_elem = A->elem;
+  a.b_elem = B->elem;
+  a.M = A->rows;
+  a.N = B->rows;
+  a.K = A->K;
+  a.act = act;
+  a.alpha = cfg ? cfg->alpha : 1.0f;
+  a.backward = backward;
+  if (a.M == 0 || a.N == 0) return MX_OK;
+  st = check_rows(out.p, out.dtype, a.N, out.ld, what, backward ? "dP" : "Y");
+  if (st == MX_OK && (r.p || backward)) st = check_rows(r.p, r.dtype, a.N, r.ld, what, backward ? "dY" : "residual");
+  if (st != MX_OK) return st;
+  if (bias && (!aligned(bias, dtype_size(bias_dtype)) || bias_stride < 0))
+    return fail(MX_ERR_INVALID_ARG, "%s: bias must be aligned to its element size, its stride >= 0", what);
+  a.out = const_cast<void*>(out.p);
+  a.ldo = out.ld;
+  a.out_bf16 = out.dtype == MX_DT_BF16;
+  a.dH = r.p;
+  a.lddh = r.p ? r.ld : 0;
+  a.dh_bf16 = r.p && r.dtype == MX_DT_BF16;
+  a.bias = bias;
+  a.bias_bf16 = bias && bias_dtype == MX_DT_BF16;
+  a.bias_stride = bias ? bias_stride : 0;
+  return MX_OK;
+}
+
+}  // namespace
+
+mx_status mx_linear(const mx_tensor* A, const mx_tensor* B, const mx_epilogue_cfg* cfg, const void* bias,
+                    int32_t bias_dtype, const void* residual, int32_t r_dtype, int64_t ldr, void* Y, int32_t y_dtype,
+                    int64_t ldy, void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_linear";
+  mx::GatedArgs a;
+  mx_status st = linear_args(A, B, cfg, bias, bias_dtype, 0, false, {residual, r_dtype, ldr}, {Y, y_dtype, ldy}, what, a);
+  if (st != MX_OK) return st;
+  return hip_status(mx::launch_linear(a, static_cast<hipStream_t>(stream)), what);
+}
+
+mx_status mx_linear_backward(const mx_tensor* A, const mx_tensor* B, const mx_epilogue_cfg* cfg, const void* bias,
+                             int32_t bias_dtype, const void* dY, int32_t dy_dtype, int64_t lddy, void* dP,
+                             int32_t dp_dtype, int64_t lddp, void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_linear_backward";
+  mx::GatedArgs a;
+  mx_status st = linear_args(A, B, cfg, bias, bias_dtype, 0, true, {dY, dy_dtype, lddy}, {dP, dp_dtype, lddp}, what, a);
+  if (st != MX_OK) return st;
+  return hip_status(mx::launch_linear(a, static_cast<hipStream_t>(stream)), what);
+}
+
+mx_status mx_grouped_linear(const mx_tensor* A, const int32_t* d_group_offsets, int32_t E, const mx_tensor* B,
+                            int64_t expert_stride_codes, int64_t expert_stride_scales, const mx_epilogue_cfg* cfg,
+                            const void* bias, int32_t bias_dtype, int64_t bias_stride, const void* residual,
+                            int32_t r_dtype, int64_t ldr, void* Y, int32_t y_dtype, int64_t ldy, void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_grouped_linear";
+  mx::GatedArgs a;
+  mx_status st = linear_args(A, B, cfg, bias, bias_dtype, bias_stride, false, {residual, r_dtype, ldr},
+                             {Y, y_dtype, ldy}, what, a);
+  if (st == MX_OK) st = gated_groups(a, A, d_group_offsets, E, expert_stride_codes, expert_stride_scales, what);
+  if (st != MX_OK) return st;
+  return hip_status(mx::launch_linear(a, static_cast<hipStream_t>(stream)), what);
+}
+
+mx_status mx_grouped_linear_backward(const mx_tensor* A, const int32_t* d_group_offsets, int32_t E, const mx_tensor* B,
+                                     int64_t expert_stride_codes, int64_t expert_stride_scales,
+                                     const mx_epilogue_cfg* cfg, const void* bias, int32_t bias_dtype,
+                                     int64_t bias_stride, const void* dY, int32_t dy_dtype, int64_t lddy, void* dP,
+                                     int32_t dp_dtype, int64_t lddp, void* stream) {
+  g_err[0] = '\0';
+  const char* what = "mx_grouped_linear_backward";
+  mx::GatedArgs a;
+  mx_status st = linear_args(A, B, cfg, bias, bias_dtype, bias_stride, true, {dY, dy_dtype, lddy}, {dP, dp_dtype, lddp},
+                             what, a);
+  if (st == MX_OK) st = gated_groups(a, A, d_group_offsets, E, expert_stride_codes, expert_stride_scales, what);
+  if (st != MX_OK) return st;
+  return hip_status(mx::launch_linear(a, static_cast<hipStream_t>(stream)), what);
+}
+
 }  // extern "C"
