@@ -28,9 +28,10 @@ CFLAGS = [
     "-ffp-contract=off", "-Wall", "-Wno-unused-function",
 ]
 # (those that take longest to compile first)
-SOURCES = ["gemm.hip", "linear_f8.hip", "linear_f8_backward.hip", "gated_f8.hip", "linear256.hip", "gated256.hip",
-           "linear.hip", "gated.hip", "mx_api.cpp", "quantize.hip", "dequantize.hip", "transpose.hip",
-           "gemm_splitk.hip", "clip.hip", "norm.hip", "dropout.hip", "experts.hip", "combine.hip", "bias_grad.hip"]
+SOURCES = ["gemm.hip", "linear_f8.hip", "linear_f8_fp6.hip", "linear_f8_backward.hip", "linear_f8_backward_fp6.hip",
+           "gated_f8.hip", "linear256_act.hip", "gated256.hip", "linear.hip", "gated.hip", "linear256.hip", "mx_api.cpp",
+           "quantize.hip", "dequantize.hip", "transpose.hip", "gemm_splitk.hip", "clip.hip", "norm.hip", "dropout.hip",
+           "experts.hip", "combine.hip", "bias_grad.hip"]
 
 
 def _run(cmd):

@@ -349,7 +349,7 @@ __device__ __forceinline__ void run_f8(const Sched& sc, const MxOperand& A, cons
         t256::store_tile_gate<false, t256c::B_INTERLEAVED>(acc, q, c0, n0, mlim, nlim);
       }
     } else if constexpr (LINEAR) {
-      t256::store_tile_linear<OUT == 5>(acc, t256c::load_gate_out(lo), c0, n0, mlim, nlim, ex);
+      t256::store_tile_linear<t256::ACT_ANY, OUT == 5>(acc, t256c::load_gate_out(lo), c0, n0, mlim, nlim, ex, 0u);
     } else {
       constexpr int ES = OUT_BF16 ? 2 : 4;
       t256::store_tile<OUT_BF16>(acc, static_cast<uint8_t*>(C) + (c0 * ldc + n0) * ES, (int)ldc, mlim, nlim);

@@ -591,9 +591,11 @@ __device__ __forceinline__ void store_unit(Acc& acc, const Sched& sc, int j, voi
 
 // Output kinds of run_tiles: float32, bf16, the quantizing epilogue
 // (MX_T256_SWAP = 1 only), the gated block's epilogues (forward, backward;
-// MX_T256_SWAP = 0 and a gated Sched::BMAP), or the linear layer's (MX_T256_SWAP = 0).
-constexpr int OUT_F32 = 0, OUT_BF16_ = 1, OUT_MX = 2, OUT_GATE = 3, OUT_GATE_BWD = 4, OUT_LINEAR = 5,
-              OUT_LINEAR_BWD = 6;
+// MX_T256_SWAP = 0 and a gated Sched::BMAP), or the linear layer's with an activation's
+// number added (forward, backward; MX_T256_SWAP = 0).
+constexpr int OUT_F32 = 0, OUT_BF16_ = 1, OUT_MX = 2, OUT_GATE = 3, OUT_GATE_BWD = 4, OUT_LINEAR = 16,
+              OUT_LINEAR_BWD = 32;
+constexpr int ACT_ANY = 4;                 // (of the linear epilogue) the activation is a run-time choice
 
 __device__ __forceinline__ void store_tile_mx(const Acc& acc, const QOut& q, int m0, int n0, int mlim, int nlim);
 
@@ -601,9 +603,13 @@ template <bool BWD, int BMAP>
 __device__ __forceinline__ void store_tile_gate(const Acc& acc, const t256c::GateOut& q, int64_t row0, int n0, int mlim,
                                                 int nlim);
 
-template <bool BWD>
+template <int ACT, bool BWD>
 __device__ __forceinline__ void store_tile_linear(const Acc& acc, const t256c::LinearOut& q, int64_t row0, int n0,
-                                                  int mlim, int nlim, int ex);
+                                                  int mlim, int nlim, int ex, uint32_t bias_lds);
+
+__device__ __forceinline__ void bring_bias(const t256c::LinearOut& q, int n0, int nlim, int ex, uint8_t* dst, int wave,
+                                           int lane);
+
 
 // Run this workgroup's tiles: C tile = A[m0:m0+256] * B[n0:n0+256]^T over all
 // K for each tile sc.tile(j), j < sc.count().  The stage sequence g = j * nst
@@ -639,19 +645,24 @@ __device__ __forceinline__ void run_tiles(const Sched& sc, const Strides& sd, in
   Acc acc;
   zero(acc);
   constexpr int ES = OUT == OUT_BF16_ ? 2 : 4;
-  auto store = [&](const TileInfo& ti) {
+  const int nst = (K + TK - 1) / TK;
+  // (linear epilogue) where a tile's bias is brought to while it is multiplied, if its
+  // stages leave the time
+  uint8_t* const bias_at = lds + 2 * STAGE_BYTES + 2 * SSLOT + 2048;
+  const uint32_t bias_addr = nst >= 3 ? (uint32_t)(uintptr_t)(lds_ptr_t)bias_at : 0u;
+  // (always inlined: as a call, the accumulators would go through memory)
+  auto store = [&](const TileInfo& ti) __attribute__((always_inline)) {
     if constexpr (OUT == OUT_MX)
       store_tile_mx(acc, qo, (int)ti.c_row0, ti.n0, ti.M - ti.m0, ti.N - ti.n0);
     else if constexpr (OUT >= OUT_LINEAR)
-      store_tile_linear<OUT == OUT_LINEAR_BWD>(acc, t256c::load_gate_out(lo), ti.c_row0, ti.n0, ti.M - ti.m0,
-                                               ti.N - ti.n0, ti.ex);
+      store_tile_linear<(OUT & 15), OUT >= OUT_LINEAR_BWD>(acc, t256c::load_gate_out(lo), ti.c_row0, ti.n0, ti.M - ti.m0,
+                                               ti.N - ti.n0, ti.ex, bias_addr);
     else if constexpr (GATED)
       store_tile_gate<OUT == OUT_GATE_BWD, BMAP>(acc, t256c::load_gate_out(go), ti.c_row0, ti.n0, ti.M - ti.m0, ti.N - ti.n0);
     else
       store_tile<OUT == OUT_BF16_>(acc, static_cast<uint8_t*>(C) + (ti.c_row0 * ldc + ti.n0) * ES, (int)ldc,
                                    ti.M - ti.m0, ti.N - ti.n0);
   };
-  const int nst = (K + TK - 1) / TK;
   if (nst == 0) {                           // K = 0: every tile is zero
     for (int j = 0; j < ntiles; ++j) store(sc.tile(j));
     return;
@@ -813,6 +824,12 @@ __device__ __forceinline__ void run_tiles(const Sched& sc, const Strides& sd, in
     wait_vmcnt(0);
     bare_barrier();
     if (more && !(s2 & 1)) issue_scales(rs2, psc, (kb2 + s2) >> 1, sslots + sslot2(g + 2), wave);
+    if constexpr (OUT >= OUT_LINEAR) {
+      // every wave has left the epilogue of the tile before (this stage's barrier), and
+      // two more barriers stand before the one of this tile
+      if (bias_addr && more && s2 == nst - 1)
+        bring_bias(t256c::load_gate_out(lo), t2.n0, t2.N - t2.n0, t2.ex, bias_at, wave, lane);
+    }
     // The next stage's first-step operands and scale bytes (in the very last
     // stage these reads of unused slots are harmless).
     const uint32_t next = lds_addr + (uint32_t)(((g + 1) & 1) * STAGE_BYTES);
@@ -915,12 +932,15 @@ __device__ __forceinline__ void store_subtile(const v16f& x, int i, int j, __amd
 // two whole lines, half as many store instructions as the plain layout.
 // Needs an even ldc and nlim and a 4-byte aligned tile origin (so a lane's
 // pair of columns is either wholly inside the matrix or wholly outside).
-__device__ __forceinline__ void store_bf16_rows(float x0, float x1, __amdgpu_buffer_rsrc_t r, uint32_t voff,
-                                                uint32_t soff, uint32_t sel) {
+__device__ __forceinline__ uint32_t pack_bf16_rows(float x0, float x1, uint32_t sel) {
   const uint32_t p = (uint32_t)__builtin_bit_cast(unsigned short, (__bf16)x0) |
                      ((uint32_t)__builtin_bit_cast(unsigned short, (__bf16)x1) << 16);
   const uint32_t q = (uint32_t)__builtin_amdgcn_mov_dpp((int)p, 0xB1, 0xF, 0xF, false);   // lane l ^ 1
-  __builtin_amdgcn_raw_buffer_store_b32(__builtin_amdgcn_perm(q, p, sel), r, voff, soff, 0);
+  return __builtin_amdgcn_perm(q, p, sel);
+}
+__device__ __forceinline__ void store_bf16_rows(float x0, float x1, __amdgpu_buffer_rsrc_t r, uint32_t voff,
+                                                uint32_t soff, uint32_t sel) {
+  __builtin_amdgcn_raw_buffer_store_b32(pack_bf16_rows(x0, x1, sel), r, voff, soff, 0);
 }
 
 // Two MFMA tiles side by side: x0, x1 hold row tile i of the wave's columns
@@ -1339,9 +1359,19 @@ __device__ __forceinline__ void store_tile_gate(const Acc& acc, const t256c::Gat
 
 // ------------------------------------------------------------ linear epilogue
 // The wave's 128 columns are taken as two pairs of MFMA column tiles, each pair in
-// the gated epilogue's pieces (four rows of two column tiles): a lane's bias values,
-// one per column tile, are loaded first, and r and the output travel in whole lines
-// where their layout allows it, exactly as the gated block's dH and h.
+// the gated epilogue's pieces (four rows of two column tiles); r and the output travel
+// in whole lines where their layout allows it, exactly as the gated block's dH and h.
+// The tile's bias is brought to LDS while the tile is multiplied, r in batches of two
+// pieces requested ahead of their use, past the caches (each word is read once).
+//
+// Loads and stores retire in one order, so the epilogue must not wait for a load that
+// it does not use: each layout has its own way through the whole tile, and on MXFP4
+// each activation its own kernel.  16384 x 2880 x 2880, bf16 (the plain product 73.5 us):
+// without r 78.5, with bias and r 98, SiLU 101, GELU 115; 82, 114 and 117 when layout
+// and activation were chosen piece by piece.  What r still costs is its 94 MB, which
+// all workgroups want at the same time: with every row of r the same one 76.6.
+// Touching r's lines while the tile is multiplied gained nothing (its share of an
+// XCD's L2 is all of it): 103-109.
 template <int ACT, bool BWD>
 __device__ __forceinline__ void linear_piece_act(const GateP& p, const Acc& acc, int i, int jp, int r4, const float b[2],
                                                  const GateTile& r, GateTile& y) {
@@ -1357,9 +1387,75 @@ __device__ __forceinline__ void linear_piece_act(const GateP& p, const Acc& acc,
     }
 }
 
-template <bool BWD>
+constexpr int LIN_AHEAD = 2;               // batches of r requested ahead of the one in use
+constexpr int CPOL_NT = 2;                 // (non-temporal: r is read once)
+
+// The tile's bias, straight to the 1 KiB of LDS at dst: 256 words, or 128 of two bf16.
+// False (nothing is done) without a bias or where its row does not start at a word.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t bias_rsrc(const t256c::LinearOut& q, int n0, int nlim, int ex) {
+  const int eb = q.flags & t256c::LIN_BIAS_BF16 ? 2 : 4;
+  return rsrc(static_cast<const uint8_t*>(q.bias) + (ex * q.bias_stride + n0) * eb, (uint32_t)((nlim < 256 ? nlim : 256) * eb));
+}
+__device__ __forceinline__ bool bias_words(const t256c::LinearOut& q, int ex) {
+  const int eb = q.flags & t256c::LIN_BIAS_BF16 ? 2 : 4;
+  return (((uintptr_t)q.bias + (uintptr_t)(ex * q.bias_stride * eb)) & 3) == 0;
+}
+__device__ __forceinline__ void bring_bias(const t256c::LinearOut& q, int n0, int nlim, int ex, uint8_t* dst, int wave,
+                                           int lane) {
+  if (q.bias == nullptr || !bias_words(q, ex) || wave >= 4) return;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(bias_rsrc(q, n0, nlim, ex), (lds_ptr_t)(dst + 256 * wave), 4,
+                                           (uint32_t)(256 * wave + 4 * lane), 0, 0, 0);
+}
+
+// This lane's bias at columns col + 32 j of the tile, from the LDS address the tile's
+// bias was brought to (0: from memory).  Each way uses its own words, so that the waits
+// for them stay on it.
+__device__ __forceinline__ void lane_bias(const t256c::LinearOut& q, int n0, int nlim, int ex, int col, uint32_t lds,
+                                          float b[TJ]) {
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) b[j] = 0.0f;
+  if (q.bias == nullptr) return;
+  const bool bf16 = q.flags & t256c::LIN_BIAS_BF16;
+  uint32_t w[TJ];
+  if (lds && bias_words(q, ex)) {
+    // asm reads that wait for themselves only (not for loads in flight to LDS)
+    if (bf16) {
+      asm volatile(
+          "ds_read_u16 %0, %4\n\tds_read_u16 %1, %4 offset:64\n\t"
+          "ds_read_u16 %2, %4 offset:128\n\tds_read_u16 %3, %4 offset:192\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(w[0]), "=&v"(w[1]), "=&v"(w[2]), "=&v"(w[3])
+          : "v"(lds + 2 * col)
+          : "memory");
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) b[j] = __uint_as_float(w[j] << 16);
+    } else {
+      asm volatile(
+          "ds_read_b32 %0, %4\n\tds_read_b32 %1, %4 offset:128\n\t"
+          "ds_read_b32 %2, %4 offset:256\n\tds_read_b32 %3, %4 offset:384\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(w[0]), "=&v"(w[1]), "=&v"(w[2]), "=&v"(w[3])
+          : "v"(lds + 4 * col)
+          : "memory");
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) b[j] = __uint_as_float(w[j]);
+    }
+    return;
+  }
+  const __amdgpu_buffer_rsrc_t r = bias_rsrc(q, n0, nlim, ex);
+  if (bf16) {
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) w[j] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, 2 * (col + 32 * j), 0, 0) << 16;
+  } else {
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) w[j] = __builtin_amdgcn_raw_buffer_load_b32(r, 4 * (col + 32 * j), 0, 0);
+  }
+  asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]));
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) b[j] = __uint_as_float(w[j]);
+}
+
+template <int ACT, bool BWD>
 __device__ __forceinline__ void store_tile_linear(const Acc& acc, const t256c::LinearOut& q, int64_t row0, int n0,
-                                                  int mlim, int nlim, int ex) {
+                                                  int mlim, int nlim, int ex, uint32_t bias_lds) {
   GatePlace pl = gate_place();                       // (its columns count a wave's 64)
   {
     const int wn64 = pl.col & 64;
@@ -1368,60 +1464,85 @@ __device__ __forceinline__ void store_tile_linear(const Acc& acc, const t256c::L
   }
   const int rows = mlim < 256 ? mlim : 256, cols = nlim < 256 ? nlim : 256;
   const int out_bf16 = q.flags & t256c::LIN_OUT_BF16, r_bf16 = q.flags & t256c::LIN_R_BF16;
-  const int bias_bf16 = q.flags & t256c::LIN_BIAS_BF16;
   const __amdgpu_buffer_rsrc_t ro = block_rsrc(q.out, row0, n0, q.ldo, rows, cols, out_bf16 ? 2 : 4);
   const __amdgpu_buffer_rsrc_t rr =
       q.r ? block_rsrc(q.r, row0, n0, q.ldr, rows, cols, r_bf16 ? 2 : 4) : rsrc(q.out, 0);   // (none: reads as zeros)
-  const int eb = bias_bf16 ? 2 : 4;
-  const __amdgpu_buffer_rsrc_t rb =
-      q.bias ? rsrc(static_cast<const uint8_t*>(q.bias) + (ex * q.bias_stride + n0) * eb, (uint32_t)(cols * eb))
-             : rsrc(q.out, 0);
   const bool lines = out_bf16 && ((q.ldo | cols) & 1) == 0 && ((uintptr_t)q.out & 3) == 0;
   const bool rlines = r_bf16 && ((q.ldr | cols) & 1) == 0 && ((uintptr_t)q.r & 3) == 0;
+  float b[TJ];
+  lane_bias(q, n0, nlim, ex, pl.col, bias_lds, b);
+  // batch n: half n & 1 (two pieces) of row tile i = (n >> 1) & 1 of column pair jp = 2 (n >> 2)
+  constexpr int NB = 2 * TI * (TJ / 2);
+  auto line_off = [&](int n, int ld) __attribute__((always_inline)) {
+    const int c = pl.line_col + 64 * (n >> 2);
+    return c < cols ? (uint32_t)((pl.line_row * ld + c) * 2) : OOB;
+  };
+  // piece h of batch n with its part of r
+  auto value = [&](int n, int h, const GateTile& r, GateTile& y) __attribute__((always_inline)) {
+    const int jp = 2 * (n >> 2), i = (n >> 1) & 1, r4 = 2 * (n & 1) + h;
+    __builtin_amdgcn_sched_barrier(0);               // (pieces begun side by side would not fit the registers)
+    if constexpr (ACT != ACT_ANY) linear_piece_act<ACT, BWD>(q.p, acc, i, jp, r4, b + jp, r, y);
+    else if (q.p.act == 0) linear_piece_act<0, BWD>(q.p, acc, i, jp, r4, b + jp, r, y);
+    else if (q.p.act == 1) linear_piece_act<1, BWD>(q.p, acc, i, jp, r4, b + jp, r, y);
+    else if (BWD || q.p.act == 2) linear_piece_act<2, BWD>(q.p, acc, i, jp, r4, b + jp, r, y);
+    else linear_piece_act<3, BWD>(q.p, acc, i, jp, r4, b + jp, r, y);
+  };
+  // One way through the whole tile per layout: where ways meet between the pieces, the
+  // compiler waits there for the loads that any of them has in flight, and with them
+  // for every store before.
+  if (lines && q.r && rlines) {
+    uint32_t w[LIN_AHEAD + 1][2][4];
+    auto request = [&](int n) __attribute__((always_inline)) {
 #pragma unroll
-  for (int jp = 0; jp < TJ; jp += 2) {
-    const bool line_in = pl.line_col < cols;
-    const uint32_t voff = line_in ? (uint32_t)((pl.line_row * q.ldo + pl.line_col) * 2) : OOB;
-    const uint32_t roff = line_in ? (uint32_t)((pl.line_row * q.ldr + pl.line_col) * 2) : OOB;
-    float b[2];
+      for (int k = 0; k < 8; ++k)
+        w[n % (LIN_AHEAD + 1)][k >> 2][k & 3] = __builtin_amdgcn_raw_buffer_load_b32(
+            rr, line_off(n, q.ldr), 2 * (32 * ((n >> 1) & 1) + 8 * (2 * (n & 1) + (k >> 2)) + (k & 2) + 4 * (k & 1)) * q.ldr,
+            CPOL_NT);
+    };
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t bo = (uint32_t)((pl.col + 32 * j) * eb);
-      b[j] = bias_bf16 ? __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rb, bo, 0, 0) << 16)
-                       : __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rb, bo, 0, 0));
-    }
+    for (int n = 0; n < LIN_AHEAD; ++n) request(n);
 #pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      uint32_t w[2][4];
+    for (int n = 0; n < NB; ++n) {
+      if (n + LIN_AHEAD < NB) request(n + LIN_AHEAD);
 #pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4) {
-        if (q.r && rlines && (r4 & 1) == 0) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            w[k >> 2][k & 3] = __builtin_amdgcn_raw_buffer_load_b32(
-                rr, roff, 2 * (32 * i + 8 * (r4 + (k >> 2)) + (k & 2) + 4 * (k & 1)) * q.ldr, 0);
-        }
+      for (int h = 0; h < 2; ++h) {
         GateTile r, y;
-        if (!q.r) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) r.t[j][k] = 0.0f;
-        } else if (rlines) {
-          unpack_piece(w[r4 & 1], pl.sel, r);
-        } else {
-          load_piece(r, i, r4, pl, cols, q.ldr, r_bf16, rr);
-        }
-        if (q.p.act == 0) linear_piece_act<0, BWD>(q.p, acc, i, jp, r4, b, r, y);
-        else if (q.p.act == 1) linear_piece_act<1, BWD>(q.p, acc, i, jp, r4, b, r, y);
-        else if (BWD || q.p.act == 2) linear_piece_act<2, BWD>(q.p, acc, i, jp, r4, b, r, y);
-        else linear_piece_act<3, BWD>(q.p, acc, i, jp, r4, b, r, y);
-        if (lines) store_piece_lines(y, i, r4, pl, voff, q.ldo, ro);
-        else store_piece(y, i, r4, pl, 1, 0, cols, q.ldo, out_bf16, ro);
+        unpack_piece(w[n % (LIN_AHEAD + 1)][h], pl.sel, r);
+        value(n, h, r, y);
+        store_piece_lines(y, (n >> 1) & 1, 2 * (n & 1) + h, pl, line_off(n, q.ldo), q.ldo, ro);
       }
     }
-    pl.col += 64;
-    pl.line_col += 64;
+    return;
+  }
+  GateTile zero;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) zero.t[j][k] = 0.0f;
+  if constexpr (!BWD) {
+    if (lines && !q.r) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          GateTile y;
+          value(n, h, zero, y);
+          store_piece_lines(y, (n >> 1) & 1, 2 * (n & 1) + h, pl, line_off(n, q.ldo), q.ldo, ro);
+        }
+      return;
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    GatePlace pj = pl;
+    pj.col += 64 * (n >> 2);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      GateTile r = zero, y;
+      if (q.r) load_piece(r, (n >> 1) & 1, 2 * (n & 1) + h, pj, cols, q.ldr, r_bf16, rr);
+      value(n, h, r, y);
+      store_piece(y, (n >> 1) & 1, 2 * (n & 1) + h, pj, 1, 0, cols, q.ldo, out_bf16, ro);
+    }
   }
 }
 #endif

@@ -21,7 +21,7 @@
 namespace mx {
 namespace {
 
-template <int FA, int FB, bool BWD>
+template <int FA, int FB, int OUT>
 __global__ __launch_bounds__(512, 1) void k_linear_f8(MxOperand A, MxOperand B, int M, int N, int K,
                                                      t256c::LinearOut lo, int a_2d, int b_2d, int tiles_m,
                                                      int tiles_n) {
@@ -32,10 +32,10 @@ __global__ __launch_bounds__(512, 1) void k_linear_f8(MxOperand A, MxOperand B, 
   __syncthreads();
   const DenseSched sc{A.codes, A.scales, B.codes, B.scales, M, N, tiles_m, tiles_n,
                       XcdShare((int)blockIdx.x, (int)gridDim.x, tiles_m * tiles_n)};
-  run_f8<FA, FB, BWD ? 5 : 4>(sc, A, B, K, nullptr, 0, a_2d, b_2d, slots, sws, t256::QOut{}, nullptr, 0, &slo);
+  run_f8<FA, FB, OUT>(sc, A, B, K, nullptr, 0, a_2d, b_2d, slots, sws, t256::QOut{}, nullptr, 0, &slo);
 }
 
-template <int FA, int FB, bool BWD>
+template <int FA, int FB, int OUT>
 __global__ __launch_bounds__(512, 1) void k_grouped_linear_f8(MxOperand A, MxOperand B, int64_t M_cap, int N, int K,
                                                              const int32_t* __restrict__ offsets, int E,
                                                              int64_t stride_codes, int64_t stride_scales,
@@ -54,10 +54,10 @@ __global__ __launch_bounds__(512, 1) void k_grouped_linear_f8(MxOperand A, MxOpe
   }
   __syncthreads();
   const GroupedSched sc{&prm, tab, XcdShare((int)blockIdx.x, (int)gridDim.x, total_slots * tiles_n)};
-  run_f8<FA, FB, BWD ? 5 : 4>(sc, A, B, K, nullptr, 0, 0, b_2d, slots, sws, t256::QOut{}, nullptr, 0, &slo);
+  run_f8<FA, FB, OUT>(sc, A, B, K, nullptr, 0, 0, b_2d, slots, sws, t256::QOut{}, nullptr, 0, &slo);
 }
 
-template <int FA, int FB, bool BWD>
+template <int FA, int FB, int OUT>
 hipError_t launch_f8(const GatedArgs& a, hipStream_t st) {
   const int cus = cu_count();
   const int tiles_n = (int)((a.N + 255) / 256);
@@ -66,31 +66,21 @@ hipError_t launch_f8(const GatedArgs& a, hipStream_t st) {
   const unsigned nwg = (unsigned)(tiles < cus ? tiles : cus);
   const t256c::LinearOut lo = linear_out(a);
   if (a.offsets)
-    hipLaunchKernelGGL((k_grouped_linear_f8<FA, FB, BWD>), dim3(nwg), dim3(512), 0, st, a.A, a.B, a.M, (int)a.N,
+    hipLaunchKernelGGL((k_grouped_linear_f8<FA, FB, OUT>), dim3(nwg), dim3(512), 0, st, a.A, a.B, a.M, (int)a.N,
                        (int)a.K, a.offsets, a.E, a.stride_codes, a.stride_scales, lo, (int)a.b_2d, tiles_n);
   else
-    hipLaunchKernelGGL((k_linear_f8<FA, FB, BWD>), dim3(nwg), dim3(512), 0, st, a.A, a.B, (int)a.M, (int)a.N,
+    hipLaunchKernelGGL((k_linear_f8<FA, FB, OUT>), dim3(nwg), dim3(512), 0, st, a.A, a.B, (int)a.M, (int)a.N,
                        (int)a.K, lo, (int)a.a_2d, (int)a.b_2d, (int)tiles_m, tiles_n);
   return hipGetLastError();
 }
 
-template <int FA, bool BWD>
+template <int FA, int OUT>
 hipError_t launch_f8_b(const GatedArgs& a, hipStream_t st) {
   switch (a.b_elem) {
-    case 1: return launch_f8<FA, 1, BWD>(a, st);
-    case 2: return launch_f8<FA, 2, BWD>(a, st);
-    case 3: return launch_f8<FA, 3, BWD>(a, st);
-    default: return launch_f8<FA, 4, BWD>(a, st);
-  }
-}
-
-template <bool BWD>
-hipError_t launch_f8_a(const GatedArgs& a, hipStream_t st) {
-  switch (a.a_elem) {
-    case 1: return launch_f8_b<1, BWD>(a, st);
-    case 2: return launch_f8_b<2, BWD>(a, st);
-    case 3: return launch_f8_b<3, BWD>(a, st);
-    default: return launch_f8_b<4, BWD>(a, st);
+    case 1: return launch_f8<FA, 1, OUT>(a, st);
+    case 2: return launch_f8<FA, 2, OUT>(a, st);
+    case 3: return launch_f8<FA, 3, OUT>(a, st);
+    default: return launch_f8<FA, 4, OUT>(a, st);
   }
 }
 

@@ -1,5 +1,5 @@
-// The linear layer with its epilogue on the MXFP8 / MXFP6 pipeline, forward (the
-// backward kernels are in linear_f8_backward.hip, compiled beside it).
+// The linear layer with its epilogue on the MXFP8 / MXFP6 pipeline, forward with FP8 A
+// (FP6 A and the backward pass are in files of their own, compiled beside this one).
 #include "linear_f8.h"
 
 namespace mx {
@@ -19,7 +19,12 @@ bool linear_f8_layout_ok(const GatedArgs& a) {
 }
 
 hipError_t launch_linear_f8(const GatedArgs& a, hipStream_t st) {
-  return a.backward ? launch_linear_f8_backward(a, st) : launch_f8_a<false>(a, st);
+  if (a.backward) return launch_linear_f8_backward(a, st);
+  switch (a.a_elem) {
+    case 1: return launch_f8_b<1, 4>(a, st);
+    case 2: return launch_f8_b<2, 4>(a, st);
+    default: return launch_linear_f8_fp6(a, st);
+  }
 }
 
 }  // namespace mx

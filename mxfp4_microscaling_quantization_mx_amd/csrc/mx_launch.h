@@ -324,8 +324,11 @@ hipError_t launch_gated_f8(const GatedArgs& a, hipStream_t st);
 hipError_t launch_linear(const GatedArgs& a, hipStream_t st);
 bool linear256_layout_ok(const GatedArgs& a);
 hipError_t launch_linear256(const GatedArgs& a, hipStream_t st);
+hipError_t launch_linear256_act(const GatedArgs& a, hipStream_t st);
 bool linear_f8_layout_ok(const GatedArgs& a);
 hipError_t launch_linear_f8(const GatedArgs& a, hipStream_t st);
+hipError_t launch_linear_f8_fp6(const GatedArgs& a, hipStream_t st);
 hipError_t launch_linear_f8_backward(const GatedArgs& a, hipStream_t st);
+hipError_t launch_linear_f8_backward_fp6(const GatedArgs& a, hipStream_t st);
 
 }  // namespace mx

@@ -28,6 +28,8 @@ constexpr int mfma_fmt() {
   else return ElemT<F>::MFMA;
 }
 
+constexpr uint32_t PAST = 0x80000000u;           // a buffer offset past any operand (taken below 2 GiB)
+
 // One operand row as a lane sees it.
 struct OpRow {
   const uint8_t* codes;
@@ -193,6 +195,14 @@ __device__ __forceinline__ void few_rows(const GatedArgs& a, const GateP& p, int
     const int nkb = (int)(a.K / 32), pieces = (nkb + 3) / 4, per = (pieces + FW - 1) / FW;
     const int d0 = w * per, d1 = d0 + per < pieces ? d0 + per : pieces;
     v16f acc = zero16();
+    // (LIN) this thread's bias, and its first pass's residual, come while the products run
+    const int col = threadIdx.x & (TN - 1);
+    float bias = 0.0f, r_first = 0.0f;
+    if (LIN && n0 + col < a.N) {
+      bias = linear_bias(a, ex, n0 + col);
+      const int row = threadIdx.x / TN;
+      if (a.dH && row < rows) r_first = load_out(a.dH, a.dh_bf16, (row0 + row) * a.lddh + n0 + col);
+    }
     for (int d = d0; d < d1; d += FD) {
       Piece<FA> pa[FD];
       Piece<FB> pb[FD];
@@ -209,7 +219,6 @@ __device__ __forceinline__ void few_rows(const GatedArgs& a, const GateP& p, int
 #pragma unroll
     for (int r = 0; r < 16; ++r) red[w][8 * (r >> 2) + 4 * hi + (r & 3)][l32] = acc[r];
     __syncthreads();
-    const int col = threadIdx.x & (TN - 1);
 #pragma unroll 1
     for (int r0 = 0; r0 < 32; r0 += 64 * FW / TN) {
       const int row = r0 + threadIdx.x / TN;
@@ -218,9 +227,8 @@ __device__ __forceinline__ void few_rows(const GatedArgs& a, const GateP& p, int
         float x = red[0][row][col];
 #pragma unroll
         for (int i = 1; i < FW; ++i) x = x + red[i][row][col];
-        const float r = a.dH ? load_out(a.dH, a.dh_bf16, (row0 + row) * a.lddh + n0 + col) : 0.0f;
-        store_out(a.out, a.out_bf16, (row0 + row) * a.ldo + n0 + col,
-                  linear_out(a, p, x + linear_bias(a, ex, n0 + col), r));
+        const float r = r0 == 0 || !a.dH ? r_first : load_out(a.dH, a.dh_bf16, (row0 + row) * a.lddh + n0 + col);
+        store_out(a.out, a.out_bf16, (row0 + row) * a.ldo + n0 + col, linear_out(a, p, x + bias, r));
         continue;
       }
       float g = red[0][row][col], u = red[0][row][col + 16];
@@ -263,21 +271,72 @@ __device__ __forceinline__ void finish16(const GatedArgs& a, const GateP& p, int
   }
 }
 
-// The same of the linear layer: x the sums of products of column c.
+// The outputs of two MFMA tiles of the linear layer side by side: rows as above, columns
+// c and c + 32, x their sums of products.  Every element is loaded and stored through
+// bounds-checked buffers, all of them requested before the first is used and with no
+// choice between them (a type chosen per element makes 32 waits: 34 us for 25 at 1037 x
+// 1451 x 2912).
 template <int ACT>
-__device__ __forceinline__ void finish16_linear(const GatedArgs& a, const GateP& p, int64_t row0, int at, int rows,
-                                                uint32_t c, int ex, int hi, const v16f& x) {
-  if (c >= (uint32_t)a.N) return;
-  char* const out = static_cast<char*>(a.out) + row0 * a.ldo * (a.out_bf16 ? 2 : 4);
-  const char* const dh = static_cast<const char*>(a.dH) + row0 * a.lddh * (a.dh_bf16 ? 2 : 4);
-  const uint32_t ld = (uint32_t)a.ldo, ldh = (uint32_t)a.lddh;
-  const float b = linear_bias(a, ex, c);
+__device__ __forceinline__ void finish_linear(const GatedArgs& a, const GateP& p, int64_t row0, int at, int rows,
+                                              uint32_t c, int ex, int hi, const v16f x[2]) {
+  auto rsrc = [&](const void* base, int64_t ld, int es) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(base)) + row0 * ld * es, 0,
+                                             (uint32_t)(((rows - 1) * ld + a.N) * es), 0x00020000);
+  };
+  const uint32_t first = (uint32_t)(at + 4 * hi);
+  // (rows past the tile's lie past its buffer, which ends with its last row)
+  auto offset = [&](int j, int r, uint32_t ld, int es) {
+    const uint32_t row = first + 8 * (r >> 2) + (r & 3);
+    return c + 32 * j < (uint32_t)a.N ? (row * ld + c + 32 * j) * es : PAST;
+  };
+  uint32_t w[2][16];
+  float b[2] = {0.0f, 0.0f};
+  if (a.bias) {
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int row = at + 8 * (r >> 2) + 4 * hi + (r & 3);
-    if (row >= rows) continue;
-    const float res = a.dH ? load_out(dh, a.dh_bf16, row * ldh + c) : 0.0f;
-    store_out(out, a.out_bf16, row * ld + c, linear_value<ACT>(p, a.backward, x[r] + b, res));
+    for (int j = 0; j < 2; ++j) b[j] = linear_bias(a, ex, c + 32 * j < (uint32_t)a.N ? c + 32 * j : a.N - 1);
+  }
+  const uint32_t ldr = (uint32_t)a.lddh, ldo = (uint32_t)a.ldo;
+  if (!a.dH) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) w[j][r] = 0u;
+  } else if (a.dh_bf16) {
+    const __amdgpu_buffer_rsrc_t rr = rsrc(a.dH, a.lddh, 2);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        w[j][r] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rr, offset(j, r, ldr, 2), 0, 0)
+                  << 16;
+  } else {
+    const __amdgpu_buffer_rsrc_t rr = rsrc(a.dH, a.lddh, 4);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        w[j][r] = __builtin_amdgcn_raw_buffer_load_b32(rr, offset(j, r, ldr, 4), 0, 0);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      w[j][r] = __float_as_uint(linear_value<ACT>(p, a.backward, x[j][r] + b[j], __uint_as_float(w[j][r])));
+  if (a.out_bf16) {
+    const __amdgpu_buffer_rsrc_t ro = rsrc(a.out, a.ldo, 2);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (__bf16)__uint_as_float(w[j][r])), ro,
+                                              offset(j, r, ldo, 2), 0, 0);
+  } else {
+    const __amdgpu_buffer_rsrc_t ro = rsrc(a.out, a.ldo, 4);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        __builtin_amdgcn_raw_buffer_store_b32(w[j][r], ro, offset(j, r, ldo, 4), 0, 0);
   }
 }
 
@@ -296,7 +355,6 @@ __device__ __forceinline__ void finish16_linear(const GatedArgs& a, const GateP&
 typedef __attribute__((address_space(3))) void* lds_ptr;
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v2i __attribute__((ext_vector_type(2)));
-constexpr uint32_t PAST = 0x80000000u;           // a buffer offset past any operand (taken below 2 GiB)
 
 template <int F>
 struct TileOp {
@@ -533,14 +591,11 @@ __device__ __forceinline__ void row_tiles(const GatedArgs& a, const GateP& p, in
       for (int r = 0; r < 16; ++r) gu[j][r] = (wk ? acc[1][j][r] : acc[0][j][r]) + red[wave ^ 4][j][r][lane];
     const int sub = 64 * wm + 32 * wk;
     if constexpr (LIN) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t c = (uint32_t)n0 + 64 * wn + 32 * j + l32;
-        if (p.act == 0) finish16_linear<0>(a, p, row0, sub, rows, c, ex, hi, gu[j]);
-        else if (p.act == 1) finish16_linear<1>(a, p, row0, sub, rows, c, ex, hi, gu[j]);
-        else if (p.act == 2) finish16_linear<2>(a, p, row0, sub, rows, c, ex, hi, gu[j]);
-        else finish16_linear<3>(a, p, row0, sub, rows, c, ex, hi, gu[j]);
-      }
+      const uint32_t c = (uint32_t)n0 + 64 * wn + l32;
+      if (p.act == 0) finish_linear<0>(a, p, row0, sub, rows, c, ex, hi, gu);
+      else if (p.act == 1) finish_linear<1>(a, p, row0, sub, rows, c, ex, hi, gu);
+      else if (p.act == 2) finish_linear<2>(a, p, row0, sub, rows, c, ex, hi, gu);
+      else finish_linear<3>(a, p, row0, sub, rows, c, ex, hi, gu);
       __syncthreads();                // the LDS is free again
       continue;
     }
