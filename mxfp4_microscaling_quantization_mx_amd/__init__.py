@@ -21,6 +21,7 @@ and, around the products of a feed-forward block,
     y = dropout(x, 0.1, seed=1, residual=r)
 """
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -684,8 +685,17 @@ class Router:
     renormalize: bool = True
     scale: float = 1.0
 
-    def c_struct(self):
+    @functools.cached_property
+    def _cfg(self):                             # (the library only reads it)
         return RouterCfgC(_SCORE[self.score], int(self.renormalize), self.scale)
+
+    def c_struct(self):
+        return self._cfg
+
+
+@functools.lru_cache(maxsize=64)
+def _epilogue_cfg(act, alpha):
+    return EpilogueCfgC(_EPILOGUE_ACT[act], alpha)
 
 
 def _slots(t, what, dtype, shape=None):
@@ -849,7 +859,7 @@ def _linear(what, a, b, offsets, bias, act, alpha, r, r_name, out_dtype, out):
         out, ldo = a.codes.new_empty(shape, dtype=out_dtype), N
     else:
         ldo = _check_rows(out, f"{what}: out", shape)
-    at, cfg = a.c_struct(), EpilogueCfgC(_EPILOGUE_ACT[act], alpha)
+    at, cfg = a.c_struct(), _epilogue_cfg(act, alpha)
     _check(getattr(lib, what)(ctypes.byref(at), *group, ctypes.byref(cfg), *epilogue, _ptr(r), rd, ldr, _ptr(out),
                               _DTYPE[out.dtype], ldo, st))
     return out

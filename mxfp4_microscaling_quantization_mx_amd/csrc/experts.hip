@@ -27,9 +27,9 @@
 // number, so its rank is a bit count and the lowest such lane alone moves the
 // wave's counter: no atomics in the ranks, the same order on every run.  One
 // workgroup takes up to one chunk in a single launch; more chunks are first
-// counted by one launch and placed by another, each workgroup of which sums the
-// counts of the chunks before its own (past SORT_DIRECT chunks a launch between
-// them turns the counts into running sums).
+// counted by one launch and placed by another, each workgroup of which adds up the
+// counts of all chunks in LDS (past SORT_DIRECT chunks a launch between them turns the
+// counts into running sums).
 #include "mx_device.h"
 #include "mx_launch.h"
 
@@ -346,8 +346,18 @@ __global__ __launch_bounds__(64 * SORT_WAVES) void k_sort_place(SortArgs a, int 
   int id[SORT_ROUNDS], at[SORT_ROUNDS];
 #pragma unroll
   for (int r = 0; r < SORT_ROUNDS; ++r) id[r] = s0 + 64 * r < a.n ? a.ids[s0 + 64 * r] : -1;
+  // the counts of all chunks, one per thread (the first of them requested here, beside
+  // the ids): SORT_DIRECT * E of them at most
+  const int counts = a.chunks > 1 && !scanned ? (int)a.chunks * a.E : 0;
+  const int first = (int)threadIdx.x < counts ? a.ws[threadIdx.x] : 0;
   for (int e = lane; e < a.E; e += 64) cnt[w][e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += nt) base[e] = tot[e] = 0;
   __syncthreads();
+  for (int i = threadIdx.x, v = first; i < counts; v = (i += nt) < counts ? a.ws[i] : 0) {
+    const int c = i / a.E, e = i - c * a.E;
+    atomicAdd(&tot[e], v);                         // (whole numbers: any order gives the same sum)
+    if (c < chunk) atomicAdd(&base[e], v);
+  }
   // each slot's rank among its expert's in this wave, and the wave's counts
 #pragma unroll
   for (int r = 0; r < SORT_ROUNDS; ++r) {
@@ -368,21 +378,12 @@ __global__ __launch_bounds__(64 * SORT_WAVES) void k_sort_place(SortArgs a, int 
       cnt[i][e] = (uint16_t)run;
       run += c;
     }
-    int pre = 0, all = run;
-    if (a.chunks > 1) {
-      if (scanned) {
-        pre = a.ws[chunk * a.E + e];
-        all = a.ws[a.chunks * a.E + e];
-      } else {
-        all = 0;
-        for (int64_t c = 0; c < a.chunks; ++c) {
-          if (c == chunk) pre = all;
-          all += a.ws[c * a.E + e];
-        }
-      }
+    if (scanned) {
+      base[e] = a.ws[chunk * a.E + e];
+      tot[e] = a.ws[a.chunks * a.E + e];
+    } else if (counts == 0) {
+      tot[e] = run;
     }
-    base[e] = pre;
-    tot[e] = all;
   }
   __syncthreads();
   if (w == 0) {                                    // group offsets: the exclusive sum of the totals
