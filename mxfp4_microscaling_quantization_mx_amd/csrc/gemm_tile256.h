@@ -1391,18 +1391,19 @@ constexpr int LIN_AHEAD = 2;               // batches of r requested ahead of th
 constexpr int CPOL_NT = 2;                 // (non-temporal: r is read once)
 
 // The tile's bias, straight to the 1 KiB of LDS at dst: 256 words, or 128 of two bf16.
-// False (nothing is done) without a bias or where its row does not start at a word.
+// Nothing is done without a bias, or where its row does not consist of whole words.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t bias_rsrc(const t256c::LinearOut& q, int n0, int nlim, int ex) {
   const int eb = q.flags & t256c::LIN_BIAS_BF16 ? 2 : 4;
   return rsrc(static_cast<const uint8_t*>(q.bias) + (ex * q.bias_stride + n0) * eb, (uint32_t)((nlim < 256 ? nlim : 256) * eb));
 }
-__device__ __forceinline__ bool bias_words(const t256c::LinearOut& q, int ex) {
+__device__ __forceinline__ bool bias_words(const t256c::LinearOut& q, int nlim, int ex) {
   const int eb = q.flags & t256c::LIN_BIAS_BF16 ? 2 : 4;
-  return (((uintptr_t)q.bias + (uintptr_t)(ex * q.bias_stride * eb)) & 3) == 0;
+  return (((uintptr_t)q.bias + (uintptr_t)(ex * q.bias_stride * eb) + (uintptr_t)((nlim < 256 ? nlim : 256) * eb)) & 3) == 0 &&
+         (((uintptr_t)q.bias + (uintptr_t)(ex * q.bias_stride * eb)) & 3) == 0;
 }
 __device__ __forceinline__ void bring_bias(const t256c::LinearOut& q, int n0, int nlim, int ex, uint8_t* dst, int wave,
                                            int lane) {
-  if (q.bias == nullptr || !bias_words(q, ex) || wave >= 4) return;
+  if (q.bias == nullptr || !bias_words(q, nlim, ex) || wave >= 4) return;
   __builtin_amdgcn_raw_ptr_buffer_load_lds(bias_rsrc(q, n0, nlim, ex), (lds_ptr_t)(dst + 256 * wave), 4,
                                            (uint32_t)(256 * wave + 4 * lane), 0, 0, 0);
 }
@@ -1417,7 +1418,7 @@ __device__ __forceinline__ void lane_bias(const t256c::LinearOut& q, int n0, int
   if (q.bias == nullptr) return;
   const bool bf16 = q.flags & t256c::LIN_BIAS_BF16;
   uint32_t w[TJ];
-  if (lds && bias_words(q, ex)) {
+  if (lds && bias_words(q, nlim, ex)) {
     // asm reads that wait for themselves only (not for loads in flight to LDS)
     if (bf16) {
       asm volatile(

@@ -64,15 +64,30 @@ hipError_t launch_direct_b(const GatedArgs& a, bool few, hipStream_t st) {
 
 }  // namespace
 
-// Which kernel: as for the gated block (launch_gated), whose tiles hold as many weight
-// rows for half as many columns.
+// Which kernel (us as k_linear_few / k_linear_tile / pipeline, N = K = 2880 unless said,
+// bias and residual, graph replays; MXFP4, then MXFP8):
+//  * k_linear_few while its workgroups are at most 2 per CU: 1 row 5.1 / 13.2 / 25 (7.2 /
+//    17.7 / 51), 128 rows 11.7 / 13.4 (17.6 / 19.6), 128 of 4096 x 4096 15.5 / 19.8 (23.3 /
+//    25.9); 192 rows 16.9 / 13.9 (24.1 / 19.2), 64 of 11264 x 4096 25.9 / 18.2 (37.6 /
+//    23.9).  Grouped over 32 experts 16 rows 16.0 / 16.7 (27.1 / 22.7), 64 rows 41.3 / 41.5
+//    (65 / 57), 256 rows 59 / 50 (90 / 69).
+//  * k_linear_tile while one workgroup per CU does in MXFP4, two with wider elements: 1280
+//    rows 19.5 / 28.0, 1400 33.1 / 28.3; 2048 rows (39.7 / 55.2), 3000 (58.5 / 56.0).  Grouped
+//    in MXFP4 up to 16 rows per expert (32 experts: 512 rows 53.4 / 57.5, 768 63.8 / 58.3; 128
+//    of 1024 x 2048: 1024 rows 50 / 46, 8192 73 / 64) or 5 workgroups per 4 CUs (8 of 4096 x
+//    4096: 256 rows 21.3 / 30.7, 1024 39 / 32), up to 128 with wider elements (32 experts:
+//    2048 rows 94 / 114, 4096 119 / 118, 8192 180 / 167; 8 of 4096 x 4096: 1024 69 / 85,
+//    4096 159 / 151).  Also everything that the pipelines do not take.
+//  * the 256-row pipelines beyond.
 hipError_t launch_linear(const GatedArgs& a, hipStream_t st) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
   const int64_t cus = cu_count();
-  const int64_t few_wgs = (a.N + 31) / 32 * slot_bound(a, 32), tile_wgs = (a.N + 127) / 128 * slot_bound(a, 128);
+  const int64_t few_wgs = (a.N + 31) / 32 * slot_bound(a, 32), tile_wgs = column_tiles(a, 128) * slot_bound(a, 128);
   const bool f4 = a.a_elem == 0 && a.b_elem == 0;
-  const bool few = a.offsets ? a.M <= 8 * (int64_t)a.E || few_wgs <= 6 * cus : 2 * few_wgs <= (f4 ? 6 : 5) * cus;
-  if (!few && (a.offsets || tile_wgs > (f4 ? 1 : 2) * cus)) {
+  const bool few = few_wgs <= 2 * cus;
+  const bool tile = a.offsets ? a.M <= (f4 ? 16 : 128) * (int64_t)a.E || (f4 && 4 * tile_wgs <= 5 * cus)
+                              : tile_wgs <= (f4 ? 1 : 2) * cus;
+  if (!few && !tile) {
     if (linear256_layout_ok(a)) return launch_linear256(a, st);
     if (linear_f8_layout_ok(a)) return launch_linear_f8(a, st);
   }

@@ -145,6 +145,50 @@ def test_two_dimensional_scales(a_block, b_block, elem, M, N):
     run_case(M, N, 160, "gelu", elem, elem, a_block, b_block)
 
 
+@pytest.mark.parametrize("a_block", ["1d", "2d"])
+@pytest.mark.parametrize("bias", [F32, BF16])
+@pytest.mark.parametrize("N", [3840, 3842, 3841, 3585])
+def test_bias_of_long_products(a_block, bias, N):
+    """Tiles of enough stages that their bias is brought to LDS beside them: widths that
+    end at and inside a tile, at an odd column; a bias row that starts at an odd element."""
+    need_gpu()
+    rng = np.random.default_rng([N, 3])
+    M, K = 1088, 832
+    qa, a = operand(rng, M, K, block=a_block)
+    qb, b = operand(rng, N, K, std=0.05)
+    rows = np.array([0, 31, 255, 256, 700, 1023, 1024, 1087])
+    P, e = projections(a[rows], b)
+    for shift in (0, 1, 2):
+        banner(f"linear bias of long products {a_block} {bias} N={N} shift={shift}")
+        bt = torch.full((N + 4,), 100.0, dtype=bias, device="cuda")[shift:shift + N]
+        bt.copy_(to_dev(rng.standard_normal(N).astype(np.float32)))
+        for name in (None, "silu"):
+            ref, tol = value_ref(P, e, f64(bt), name, 1.0, None)
+            check(host(mx.linear(qa, qb, bt, name, out_dtype=F32))[rows], ref, tol, False)
+
+
+@pytest.mark.parametrize("bias", [F32, BF16])
+def test_grouped_bias_of_long_products(bias):
+    """The same per expert, bias rows a stride apart that starts them at odd elements."""
+    need_gpu()
+    rng = np.random.default_rng(17)
+    counts, N, K = [1300, 0, 900, 77], 2401, 640
+    off, qa, a, qb, bs = grouped(rng, counts, sum(counts), N, K)
+    for stride in (2401, 2402, 2404):
+        banner(f"grouped linear bias of long products {bias} stride={stride}")
+        bt = torch.zeros(4, stride, dtype=bias, device="cuda")[:, :N]
+        bt.copy_(to_dev(rng.standard_normal((4, N)).astype(np.float32)))
+        y = host(mx.grouped_linear(qa, to_dev(off), qb, bt, out_dtype=F32))
+        check_groups(off, a, bs, f64(bt), None, None, y, None, None, True)
+
+
+@pytest.mark.parametrize("elem,M,N", [("e2m1", 1120, 3808), ("e4m3", 1120, 7424)])
+@pytest.mark.parametrize("b_block", ["1d", "2d"])
+def test_two_dimensional_scales_without_an_activation(elem, M, N, b_block):
+    need_gpu()
+    run_case(M, N, 608, None, elem, elem, "2d", b_block, out=BF16, res=BF16)
+
+
 @pytest.mark.parametrize("scale_pad", [1, 2, 4])
 @pytest.mark.parametrize("ea,eb", [("e2m1", "e2m1"), ("e4m3", "e4m3"), ("e4m3", "e2m3")])
 @pytest.mark.parametrize("M,N,K", [(40, 60, 608), (420, 1800, 608), (1100, 3800, 288)])
@@ -243,18 +287,20 @@ def check_groups(off, a, bs, bias, r, dy, y, dp, name, exact, experts=None):
         lo, hi = off[e], off[e + 1]
         if lo == hi:
             continue
-        P, err = projections(a[lo:hi], bs[e], exact)
+        rows = lo + sample_rows(hi - lo, bs[e].shape[0])
+        P, err = projections(a[rows], bs[e], exact)
         be = None if bias is None else bias[e]
-        ref, tol = value_ref(P, err, be, name, 1.0, None if r is None else r[lo:hi])
-        check(y[lo:hi], ref, tol, False, what=f"y of expert {e}")
+        ref, tol = value_ref(P, err, be, name, 1.0, None if r is None else r[rows])
+        check(y[rows], ref, tol, False, what=f"y of expert {e}")
         if dp is not None:
-            ref, tol = gradient_ref(P, err, be, name, 1.0, dy[lo:hi])
-            check(dp[lo:hi], ref, tol, False, what=f"dp of expert {e}")
+            ref, tol = gradient_ref(P, err, be, name, 1.0, dy[rows])
+            check(dp[rows], ref, tol, False, what=f"dp of expert {e}")
 
 
 @pytest.mark.parametrize("counts,N,K", [
     ([0, 1, 0, 2], 48, 96), ([33, 0, 31, 1, 100], 32, 64), ([700, 0, 3, 256, 257, 0], 1184, 288), ([0, 0, 0], 16, 32),
-    ([1] * 70, 16, 64), ([300, 20], 544, 800), ([1200, 0, 900], 1600, 96)])
+    ([1] * 70, 16, 64), ([300, 20], 544, 800), ([1200, 0, 900], 1600, 96), ([1300, 0, 900, 77], 2400, 608),
+    ([513, 800], 3872, 96)])
 @pytest.mark.parametrize("ea,eb", [("e2m1", "e2m1"), ("e4m3", "e4m3"), ("e4m3", "e2m1")])
 @pytest.mark.parametrize("b_block", ["1d", "2d"])
 def test_grouped(counts, N, K, ea, eb, b_block):
@@ -365,3 +411,23 @@ def test_equal_to_the_product():
     qb, _ = operand(rng, 4100, 320)
     for dt in (F32, BF16):
         assert torch.equal(mx.linear(qa, qb, out_dtype=dt), mx.gemm(qa, qb, dt))
+
+
+def test_outputs_past_32_bits():
+    """4.4 GB of output and of residual: addresses past 32 bits."""
+    need_gpu()
+    M, N, K = 270000, 8192, 32
+    banner(f"linear {M}x{N}x{K}")
+    rng = np.random.default_rng(8)
+    qa, a = operand(rng, M, K)
+    qb, b = operand(rng, N, K)
+    bias = torch.randn(N, device="cuda")
+    r = torch.zeros(M, N, dtype=BF16, device="cuda")
+    rows = np.array([0, 1, 131071, 131072, 262143, 262144, 269999])
+    idx = torch.from_numpy(rows).cuda()
+    r[idx] = torch.randn(rows.size, N, device="cuda").to(BF16)
+    want = f64(r[idx])
+    mx.linear(qa, qb, bias, None, r, out=r)              # in place
+    P, e = projections(a[rows], b)
+    ref, tol = value_ref(P, e, f64(bias), None, 1.0, want)
+    check(host(r[idx].float()), ref, tol, True)
