@@ -698,6 +698,17 @@ def _epilogue_cfg(act, alpha):
     return EpilogueCfgC(_EPILOGUE_ACT[act], alpha)
 
 
+# (sizes alone decide these: asked once per shape)
+@functools.lru_cache(maxsize=256)
+def _sort_workspace(T, top, E):
+    return load_library().mx_expert_sort_workspace_size(T, top, E)
+
+
+@functools.lru_cache(maxsize=256)
+def _bias_grad_workspace(M, N, E):
+    return load_library().mx_bias_grad_workspace_size(M, N, E)
+
+
 def _slots(t, what, dtype, shape=None):
     """Check a contiguous [T, top] array of slots (where it is: _stream)."""
     if t.dim() != 2 or t.dtype != dtype or not t.is_contiguous():
@@ -755,7 +766,7 @@ def expert_sort(ids, E):
     T, top = ids.shape
     # (E may be refused: the library answers before it looks at the buffers)
     offsets, rows, dest = ids.new_empty(max(E, 0) + 1), ids.new_empty(T * top), ids.new_empty((T, top))
-    nbytes = lib.mx_expert_sort_workspace_size(T, top, E)
+    nbytes = _sort_workspace(T, top, E)
     ws = ids.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
     _check(lib.mx_expert_sort(_ptr(ids), T, top, E, _ptr(offsets), _ptr(rows), _ptr(dest), _ptr(ws), nbytes, st))
     return offsets, rows, dest
@@ -901,18 +912,17 @@ def bias_grad(dp, offsets=None, dtype=torch.float32):
     if dtype not in _DTYPE:
         raise ValueError("bias_grad: dtype must be bf16 or float32")
     M, N = dp.shape
+    st = _stream(dp, offsets)
     if offsets is None:
-        st = _stream(dp)
         E, group, shape, f = 1, (), (N,), lib.mx_bias_grad
     else:
         E = offsets.numel() - 1
         _check_offsets(offsets, E)
         if E < 1:
             raise ValueError("bias_grad: offsets must have at least two entries")
-        st = _stream(dp, offsets)
         group, shape, f = (_ptr(offsets), E), (E, N), lib.mx_grouped_bias_grad
-    out = dp.new_empty(shape, dtype=dtype)
-    nbytes = lib.mx_bias_grad_workspace_size(M, N, E)
+    out = dp.new_empty(shape) if dtype == dp.dtype else dp.new_empty(shape, dtype=dtype)
+    nbytes = _bias_grad_workspace(M, N, E)
     ws = dp.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
     _check(f(_ptr(dp), _DTYPE[dp.dtype], M, N, ld, *group, _ptr(out), _DTYPE[dtype], _ptr(ws), nbytes, st))
     return out
