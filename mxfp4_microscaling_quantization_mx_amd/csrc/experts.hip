@@ -19,7 +19,10 @@
 // preserving 32-bit keys; a choice is a maximum over the group (DPP), and a
 // ballot that names the lowest lane holding it.  Lane j then has the j-th chosen
 // logit and the softmax runs across the group.  Little is read (1 MB for 16384
-// tokens of 32 experts): the launch and the latency of one row bound it.
+// tokens of 32 experts): the launch and the latency of one row bound it, 3.4-4 us for
+// 16 tokens of 128 experts, 16384 of 32 and its backward pass alike (7.5 with the
+// call); 16384 of 256 experts, top 8, 10.1 us, of 1024 25.7 (1.3 TB/s: eight
+// reductions over 64 lanes).
 //
 // Sort.  A stable counting sort of the slots (token t, choice j) at 4 t + j and
 // the like: chunks of 4096 slots, 16 waves of 4 rounds of 64.  In a round every
@@ -29,7 +32,9 @@
 // workgroup takes up to one chunk in a single launch; more chunks are first
 // counted by one launch and placed by another, each workgroup of which adds up the
 // counts of all chunks in LDS (past SORT_DIRECT chunks a launch between them turns the
-// counts into running sums).
+// counts into running sums).  64 slots 3.3 us (7.9 with the call), 65536 slots of
+// 32 experts 4.2 + 5.6-6.4 us, each of the two its launch and two trips to memory;
+// 262144 of 128 experts 13.2 us, a million of 256 20.6 (three launches).
 #include "mx_device.h"
 #include "mx_launch.h"
 

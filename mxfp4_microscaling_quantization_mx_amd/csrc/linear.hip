@@ -11,8 +11,11 @@
 //  * k_linear_few: 32 rows by 32 columns per workgroup of 8 or 2 waves, which split K.
 //    For few rows, where reading the weight once with as many loads in flight as
 //    possible is all that counts.
+//    One row of N = K = 2880 5.2 us (9.0 with the call): the launch, two trips along K and
+//    one to the output for 4.2 MB.
 //  * k_linear_tile: 128 rows by 128 columns per workgroup of 8 waves, operands
-//    staged through a ring in LDS.
+//    staged through a ring in LDS.  1037 x 1451 x 2912 MXFP8 backward 21.4 us: 108
+//    workgroups of 23 stages, 0.6 us each, on 256 CUs.
 #include "product_tiles.h"
 
 namespace mx {

@@ -41,9 +41,9 @@ CALLS = {
                                     "lddy", "dw", "stream"],
                                    [P(16), 1, 4, 64, 64, P(16), 8, 64, P(16), P(16), 2, P(16), 64, P(16), None]),
     "mx_bias_grad": (["dp", "dtype", "M", "N", "ld", "out", "odtype", "ws", "nws", "stream"],
-                     [P(16), 1, 1000, 64, 64, P(16), 0, P(16), 1 << 20, None]),
+                     [P(16), 1, 2000, 64, 64, P(16), 0, P(16), 1 << 20, None]),
     "mx_grouped_bias_grad": (["dp", "dtype", "M", "N", "ld", "off", "E", "out", "odtype", "ws", "nws", "stream"],
-                             [P(16), 1, 1000, 64, 64, P(16), 3, P(16), 0, P(16), 1 << 20, None]),
+                             [P(16), 1, 2000, 64, 64, P(16), 3, P(16), 0, P(16), 1 << 20, None]),
 }
 
 
@@ -128,8 +128,8 @@ def test_workspace_sizes(lib):
     assert f(1024, 4, 32) == 0 and f(1025, 4, 32) == 3 * 32 * 4 and f(16384, 4, 32) == 17 * 32 * 4
     assert f(0, 4, 32) == f(-1, 4, 32) == f(4, 0, 32) == f(4, 4, 0) == f(4, 4, 1025) == f(BIG, 4, 32) == 0
     f = lib.mx_bias_grad_workspace_size
-    assert f(512, 2880, 32) == 0 and f(0, 8, 1) == f(8, 0, 1) == f(600, 8, 0) == f(BIG, 8, 1) == 0
-    for M, N, E in ((513, 7, 1), (1024, 64, 1), (65536, 2880, 32)):
+    assert f(1024, 2880, 32) == 0 and f(0, 8, 1) == f(8, 0, 1) == f(1100, 8, 0) == f(BIG, 8, 1) == 0
+    for M, N, E in ((1025, 7, 1), (2048, 64, 1), (65536, 2880, 32)):
         tiles = M // 256 + min(E, M)                       # a partial tile per expert at most
         assert f(M, N, E) == tiles * N * 4
 

@@ -175,25 +175,27 @@ def test_offsets_past_32_bits():
     assert bool(((dw.double() - ref).abs() <= 48 * U * mag).all())
     tail = y[rows - 4096:]
     tail.fill_(1.0)
-    got = mx.bias_grad(y[rows - 600:])                   # (addresses past 32 bits)
-    assert torch.equal(got, torch.full((C,), 600.0, device="cuda"))
+    for n in (600, 3000):                                # (addresses past 32 bits)
+        assert torch.equal(mx.bias_grad(y[rows - n:]), torch.full((C,), float(n), device="cuda"))
 
 
 # ------------------------------------------------------------------ bias gradient
 def bias_tol(ref_mag, M, E, dtype):
-    # a wave's 16 rows of a tile (512 rows in one go: 32), 4 steps over waves, then the tiles by four
-    return (32 + 4 + M / 256 / 4 + 4) * U * ref_mag + TINY
+    # a lane adds up at most 64 rows (1024 in one go, 16 waves), then 2 steps over lanes and 15
+    # over waves, then every fourth tile and the four sums
+    return (64 + 17 + M / 256 / 4 + 4) * U * ref_mag + TINY
 
 
 @pytest.mark.parametrize("N", [1, 5, 8, 255, 513, 1451, 2880])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_bias_grad(N, dtype):
     need_gpu()
-    for M in (0, 1, 2, 255, 256, 257, 512, 513, 1037, 5000):
+    for M in (0, 1, 2, 63, 64, 65, 255, 257, 1024, 1025, 1037, 5000):
         banner(f"bias grad M={M} N={N} {dtype}")
         for ld, shift in ((N, 0), (N + 3, 1)):
             x = strided((M, N), ld, shift, dtype, M)
-            ref, mag = f64(x).sum(0), np.abs(f64(x)).sum(0)
+            xd = f64(x)
+            ref, mag = xd.sum(0), np.abs(xd).sum(0)
             for out in (F32, BF16):
                 got = mx.bias_grad(x, dtype=out)
                 assert got.dtype == out and got.shape == (N,)
@@ -202,31 +204,32 @@ def test_bias_grad(N, dtype):
 
 
 @pytest.mark.parametrize("sizes", [[3], [0, 0, 5, 0], [256, 0, 512, 1], [700, 0, 1, 2000, 255, 257], [1] * 300 + [0] * 20,
-                                   [0, 0], [5000]])
+                                   [0, 0], [5000], [300, 0, 724], [20] * 256])
 def test_grouped_bias_grad(sizes):
     need_gpu()
     banner(f"grouped bias grad {sizes[:8]}")
     offsets = torch.tensor(np.cumsum([0] + sizes), dtype=torch.int32, device="cuda")
     for extra in (0, 40):                                # rows past the last group are not read
-        for N, dtype in ((100, F32), (1451, BF16)):
+        for N, dtype in ((100, F32), (1451, BF16), (2880, BF16)):
             M = sum(sizes) + extra
             x = strided((M, N), N, 0, dtype, 7)
             if extra:
                 x[sum(sizes):] = NAN
             got = mx.bias_grad(x, offsets)
             assert got.shape == (len(sizes), N)
-            ends = np.cumsum([0] + sizes)
-            ref = np.stack([f64(x)[a:b].sum(0) for a, b in zip(ends, ends[1:])])
-            mag = np.stack([np.abs(f64(x)[a:b]).sum(0) for a, b in zip(ends, ends[1:])])
+            ends, xd = np.cumsum([0] + sizes), f64(x)
+            ref = np.stack([xd[a:b].sum(0) for a, b in zip(ends, ends[1:])])
+            mag = np.stack([np.abs(xd[a:b]).sum(0) for a, b in zip(ends, ends[1:])])
             close(got, ref, bias_tol(mag, M, len(sizes), dtype))
 
 
 def test_grouped_bias_grad_clamps_offsets():
     need_gpu()
     banner("grouped bias grad offsets past the rows")
-    x = torch.ones(600, 33, device="cuda")
-    got = mx.bias_grad(x, torch.tensor([0, 500, 2**31 - 1, 2**31 - 1], dtype=torch.int32, device="cuda"))
-    assert torch.equal(got, torch.tensor([500.0, 100.0, 0.0], device="cuda")[:, None].expand(3, 33))
+    for M in (600, 1600):
+        x = torch.ones(M, 33, device="cuda")
+        got = mx.bias_grad(x, torch.tensor([-5, 500, 2**31 - 1, 2**31 - 1], dtype=torch.int32, device="cuda"))
+        assert torch.equal(got, torch.tensor([500.0, M - 500.0, 0.0], device="cuda")[:, None].expand(3, 33))
 
 
 # ------------------------------------------------------------------ streams, graphs, repeats
