@@ -127,8 +127,9 @@ __global__ __launch_bounds__(64 * BG_WAVES) void k_bias_part(BiasGradArgs a, uin
 }
 
 // blockIdx.x: 64 columns, blockIdx.y: expert.  Wave w adds the tiles w, w + 4, ...
-// and the four sums are added in order.
-__global__ __launch_bounds__(256) void k_bias_sum(BiasGradArgs a) {
+// and the four sums are added in order.  (Offsets that decrease may name more tiles
+// than the `bound` that ws holds; those past it are left out.)
+__global__ __launch_bounds__(256) void k_bias_sum(BiasGradArgs a, int64_t bound) {
   __shared__ float red[4][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
@@ -138,7 +139,8 @@ __global__ __launch_bounds__(256) void k_bias_sum(BiasGradArgs a) {
       expert_rows(a.offsets, e, a.M, lo, hi);
       s0 = slots_before<BG_ROWS>(a.offsets, e, a.M);
     }
-    const int64_t tiles = (hi - lo + BG_ROWS - 1) / BG_ROWS;
+    int64_t tiles = (hi - lo + BG_ROWS - 1) / BG_ROWS;
+    if (tiles > bound - s0) tiles = bound - s0;
     float s = 0.0f;
     if (c < a.N)
 #pragma unroll 8
@@ -165,7 +167,7 @@ hipError_t launch_bias_grad_t(const BiasGradArgs& a, hipStream_t st) {
   const int64_t tiles = tile_bound(a.M, a.E, a.offsets != nullptr);
   hipLaunchKernelGGL((k_bias_part<BF16, LPR>), dim3((unsigned)(tiles * slabs)), dim3(64 * BG_WAVES), 0, st, a,
                      (uint32_t)slabs);
-  hipLaunchKernelGGL(k_bias_sum, dim3((unsigned)((a.N + 63) / 64), ey), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(k_bias_sum, dim3((unsigned)((a.N + 63) / 64), ey), dim3(256), 0, st, a, tiles);
   return hipGetLastError();
 }
 
@@ -183,8 +185,11 @@ hipError_t launch_bias_grad_w(const BiasGradArgs& a, hipStream_t st) {
 size_t bias_grad_workspace(int64_t M, int64_t N, int32_t E, bool grouped) {
   return M <= BG_DIRECT ? 0 : (size_t)tile_bound(M, E, grouped) * (size_t)N * sizeof(float);
 }
+// (a launch has fewer than 2^32 threads along an axis, a workgroup 1024 and at least
+// 256 columns where there are many)
 bool bias_grad_fits(int64_t M, int64_t N, int32_t E, bool grouped) {
-  return tile_bound(M, E, grouped) * ((N + 63) / 64) < (1ll << 31);
+  const int64_t tiles = tile_bound(M, E, grouped);
+  return (tiles < 1 ? 1 : tiles) * ((N + 255) / 256) < (1ll << 22);
 }
 
 hipError_t launch_bias_grad(const BiasGradArgs& a, hipStream_t st) {

@@ -232,6 +232,18 @@ def test_grouped_bias_grad_clamps_offsets():
         assert torch.equal(got, torch.tensor([500.0, M - 500.0, 0.0], device="cuda")[:, None].expand(3, 33))
 
 
+def test_grouped_bias_grad_of_offsets_that_decrease():
+    """Experts that claim the same rows again name more tiles than there is room for;
+    those past it are left out, and nothing past the workspace is read."""
+    need_gpu()
+    banner("grouped bias grad offsets that decrease")
+    x = torch.ones(2000, 33, device="cuda")
+    got = mx.bias_grad(x, torch.tensor([0, 2000] * 40 + [0], dtype=torch.int32, device="cuda"))
+    assert got.shape == (80, 33)
+    assert torch.equal(got[0], torch.full((33,), 2000.0, device="cuda"))
+    assert not got[1::2].any()                           # (2000 .. 0: no rows)
+
+
 # ------------------------------------------------------------------ streams, graphs, repeats
 def test_replays_and_another_stream():
     """Captured calls replayed on changed inputs with eager work between, and eager
