@@ -657,7 +657,7 @@ typedef struct {
  *   logits   device; [T, E] of `dtype` (mx_dtype), row stride ld elements (>= E).
  *   E        1 .. 1024; top 1 .. min(E, 64) (above 64 or 1024: MX_ERR_UNSUPPORTED).
  *   ids      device; int32 [T, top].  weights: device; float32 [T, top].
- *   T = 0: nothing is written.  At most 2^31 - 1 tokens.
+ *   T = 0: nothing is written.  At most 2^26 - 4 tokens (MX_ERR_UNSUPPORTED).
  */
 mx_status mx_route(const void* logits, int32_t dtype, int64_t T, int32_t E, int64_t ld, int32_t top,
                    const mx_router_cfg* cfg, int32_t* ids, float* weights, void* stream);
@@ -717,6 +717,8 @@ size_t mx_expert_sort_workspace_size(int64_t T, int32_t top, int32_t E);
  *   xs    device; [rows, C] of `dtype`, row stride ldxs (>= C).  Rows that no entry
  *         names are left untouched; a row named twice gets one of the tokens' bytes in
  *         each of its pieces.  Must not overlap x.
+ *   At most 2^26 - 4 tokens, and KiB of x with each row rounded up (MX_ERR_UNSUPPORTED;
+ *   the two calls below alike).
  */
 mx_status mx_expert_dispatch(const void* x, int32_t dtype, int64_t T, int64_t C, int64_t ldx, const int32_t* dest,
                              int32_t top, void* xs, int64_t rows, int64_t ldxs, void* stream);
@@ -730,7 +732,8 @@ mx_status mx_expert_dispatch(const void* x, int32_t dtype, int64_t T, int64_t C,
  *   dest      device; int32 [T, top].
  *   weights   device; float32 [T, top]; NULL = 1 (the gradient of a dispatch).
  *   residual  device; [T, C] of `dtype`, row stride ldr; NULL = none.
- *   out       device; [T, C] of `dtype`, row stride ldo.  May be residual itself.
+ *   out       device; [T, C] of `dtype`, row stride ldo.  May be residual itself;
+ *             must not overlap y.
  */
 mx_status mx_expert_combine(const void* y, int32_t dtype, int64_t rows, int64_t C, int64_t ldy, const int32_t* dest,
                             const float* weights, int64_t T, int32_t top, const void* residual, int64_t ldr, void* out,
@@ -826,7 +829,8 @@ mx_status mx_grouped_linear_backward(const mx_tensor* A, const int32_t* d_group_
  *   workspace  device, 4-byte aligned, mx_bias_grad_workspace_size(M, N, E) bytes
  *              (E = 1 for mx_bias_grad; NULL where that is 0); contents before and
  *              after are of no meaning.
- *   N = 0: nothing is written.  M = 0 writes zeros.
+ *   N = 0: nothing is written.  M = 0 writes zeros.  Tiles of 256 rows (and one partial
+ *   tile per expert) by 256 columns: at most 2^22 - 1 (MX_ERR_UNSUPPORTED).
  */
 mx_status mx_bias_grad(const void* dp, int32_t dtype, int64_t M, int64_t N, int64_t ld, void* out, int32_t out_dtype,
                        void* workspace, size_t ws_bytes, void* stream);

@@ -299,6 +299,13 @@ __device__ __forceinline__ uint64_t same_expert(int id, bool live, int bits) {
   return m;
 }
 
+// LDS accesses of one wave keep this order (the hardware takes them in turn; this holds
+// the compiler to it).
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Slots of chunk blockIdx.x per expert: ws[chunk][E].
 __global__ __launch_bounds__(64 * SORT_WAVES) void k_sort_count(SortArgs a) {
   __shared__ int cnt[SORT_EMAX];
@@ -371,9 +378,9 @@ __global__ __launch_bounds__(64 * SORT_WAVES) void k_sort_place(SortArgs a, int 
     const int before = __popcll(m & ((1ull << lane) - 1));
     const int seen = live ? cnt[w][id[r]] : 0;
     at[r] = seen + before;
-    __builtin_amdgcn_wave_barrier();               // (all lanes have read before the first one writes)
+    wave_fence();                                  // all lanes have read before the first one writes
     if (live && before == 0) cnt[w][id[r]] = (uint16_t)(seen + __popcll(m));
-    __builtin_amdgcn_wave_barrier();
+    wave_fence();
   }
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += nt) {

@@ -923,6 +923,7 @@ mx_status mx_dropout(const void* x, int32_t dtype, int64_t R, int64_t C, int64_t
 namespace {
 
 constexpr int32_t EXPERTS_MAX = 1024, CHOICES_MAX = 64;
+constexpr int64_t WAVES_MAX = (1 << 26) - 4;   // a launch has fewer than 2^32 threads, 256 per workgroup
 
 mx_status router_args(const void* logits, int32_t dtype, int64_t T, int32_t E, int64_t ld, int32_t top,
                       const mx_router_cfg* cfg, const char* what, mx::RouteArgs& a) {
@@ -936,8 +937,8 @@ mx_status router_args(const void* logits, int32_t dtype, int64_t T, int32_t E, i
   if (T < 0) return fail(MX_ERR_INVALID_ARG, "%s: negative shape", what);
   if (E < 1) return fail(MX_ERR_INVALID_ARG, "%s: E=%d < 1", what, E);
   if (top < 1 || top > E) return fail(MX_ERR_INVALID_ARG, "%s: top=%d is not in 1 .. E=%d", what, top, E);
-  if (E > EXPERTS_MAX || top > CHOICES_MAX || T > 0x7FFFFFFF)
-    return fail(MX_ERR_UNSUPPORTED, "%s: at most %d experts, %d choices and 2^31 - 1 tokens", what, EXPERTS_MAX,
+  if (E > EXPERTS_MAX || top > CHOICES_MAX || T > WAVES_MAX)
+    return fail(MX_ERR_UNSUPPORTED, "%s: at most %d experts, %d choices and 2^26 - 4 tokens", what, EXPERTS_MAX,
                 CHOICES_MAX);
   if (T == 0) return MX_OK;
   mx_status st = check_rows(logits, dtype, E, ld, what, "logits");
@@ -967,8 +968,9 @@ mx_status combine_args(int32_t dtype, int64_t T, int64_t C, int64_t rows, int32_
   if (!known_dtype(dtype)) return fail(MX_ERR_INVALID_ARG, "%s: unknown dtype %d", what, dtype);
   if (T < 0 || C < 0 || rows < 0) return fail(MX_ERR_INVALID_ARG, "%s: negative shape", what);
   if (top < 1) return fail(MX_ERR_INVALID_ARG, "%s: top=%d < 1", what, top);
-  // (a wave per row at least; 64 pieces of 4 elements per wave)
-  if (T > 0x7FFFFFFF || C > 0x7FFFFFFF || T * ((C + 255) / 256) > 0x7FFFFFFF)
+  // (at most a wave per 64 pieces of 16 bytes of a row, and for a row)
+  const int64_t piece = 64 * 16 / (int64_t)dtype_size(dtype);
+  if (T > WAVES_MAX || C > 0x7FFFFFFF || T * ((C + piece - 1) / piece) > WAVES_MAX)
     return fail(MX_ERR_UNSUPPORTED, "%s: too many rows or columns", what);
   if (T && C) {
     mx_status st = check_words(dest, what, "dest");

@@ -63,7 +63,8 @@ REFUSED = [
     ("mx_route", BAD, dict(cfg=None)), ("mx_route", BAD, dict(cfg=_router(2))), ("mx_route", BAD, dict(cfg=_router(0, 2))),
     ("mx_route", BAD, dict(cfg=_router(scale=NAN))), ("mx_route", BAD, dict(cfg=_router(scale=INF))),
     ("mx_route", UNSUP, dict(E=1025, ld=1025)), ("mx_route", UNSUP, dict(E=128, ld=128, top=65)),
-    ("mx_route", UNSUP, dict(T=BIG)),
+    ("mx_route", UNSUP, dict(T=BIG)), ("mx_route", UNSUP, dict(T=2**26 - 3)),
+    ("mx_route_backward", UNSUP, dict(T=2**26 - 3)),
     ("mx_route_backward", BAD, dict(dw=None)), ("mx_route_backward", BAD, dict(dw=P(18))),
     ("mx_route_backward", BAD, dict(ids=None)), ("mx_route_backward", BAD, dict(dx=None)),
     ("mx_route_backward", BAD, dict(ldd=31)), ("mx_route_backward", BAD, dict(dx=P(17))),
@@ -83,6 +84,9 @@ REFUSED = [
     ("mx_expert_dispatch", BAD, dict(ldx=63)), ("mx_expert_dispatch", BAD, dict(ldxs=63)),
     ("mx_expert_dispatch", BAD, dict(xs=P(17))), ("mx_expert_dispatch", UNSUP, dict(T=BIG)),
     ("mx_expert_dispatch", UNSUP, dict(T=1 << 30, C=1024, ldx=1024, ldxs=1024)),
+    ("mx_expert_dispatch", UNSUP, dict(T=2**26 - 3)), ("mx_expert_combine", UNSUP, dict(T=2**26 - 3)),
+    ("mx_expert_combine", UNSUP, dict(T=2**25, C=513, ldy=513, ldr=513, ldo=513)),
+    ("mx_expert_combine_backward", UNSUP, dict(dtype=0, T=2**25, C=257, ldy=257, lddo=257, lddy=257)),
     ("mx_expert_combine", BAD, dict(dtype=2)), ("mx_expert_combine", BAD, dict(rows=-1)),
     ("mx_expert_combine", BAD, dict(top=0)), ("mx_expert_combine", BAD, dict(y=None)),
     ("mx_expert_combine", BAD, dict(y=P(17))), ("mx_expert_combine", BAD, dict(ldy=63)),
@@ -99,7 +103,8 @@ REFUSED = [
     ("mx_bias_grad", BAD, dict(N=-1)), ("mx_bias_grad", BAD, dict(dp=None)), ("mx_bias_grad", BAD, dict(dp=P(17))),
     ("mx_bias_grad", BAD, dict(ld=63)), ("mx_bias_grad", BAD, dict(out=None)), ("mx_bias_grad", BAD, dict(out=P(18))),
     ("mx_bias_grad", BAD, dict(ws=None)), ("mx_bias_grad", BAD, dict(ws=P(18))), ("mx_bias_grad", BAD, dict(nws=64)),
-    ("mx_bias_grad", UNSUP, dict(M=BIG)),
+    ("mx_bias_grad", UNSUP, dict(M=BIG)), ("mx_bias_grad", UNSUP, dict(M=2**30)),
+    ("mx_bias_grad", UNSUP, dict(M=0, N=2**30, ld=2**30)), ("mx_grouped_bias_grad", UNSUP, dict(M=2**30 - 512)),
     ("mx_grouped_bias_grad", BAD, dict(off=None)), ("mx_grouped_bias_grad", BAD, dict(off=P(18))),
     ("mx_grouped_bias_grad", BAD, dict(E=0)), ("mx_grouped_bias_grad", BAD, dict(nws=64)),
 ]
