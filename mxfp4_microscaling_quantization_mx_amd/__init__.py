@@ -19,6 +19,19 @@ and, around the products of a feed-forward block,
     y, mean, rstd = layer_norm(x, weight, bias)
     dx, dw, db = layer_norm_backward(dy, x, mean, rstd, weight)
     y = dropout(x, 0.1, seed=1, residual=r)
+    y = linear(qa, qb, bias, act="gelu", residual=r)    # act(A * B^T + bias) + r
+    dp = linear_backward(qa, qb, dy, bias, act="gelu")
+    db = bias_grad(dp)
+
+and, around the grouped products of an expert layer,
+
+    ids, weights = route(logits, top, Router())
+    offsets, rows, dest = expert_sort(ids, E)           # for grouped_*, quantize_gather, quantize_scatter
+    xs = expert_dispatch(x, dest)
+    ys = grouped_linear(qxs, offsets, qw, bias, act="gelu")
+    y = expert_combine(ys, dest, weights, residual=x)
+    dys, dweights = expert_combine_backward(dy, ys, dest, weights)
+    dlogits = route_backward(dweights, logits, ids, Router())
 """
 import ctypes
 import functools
