@@ -8,11 +8,9 @@
 // The kernels here take any shape, element types, scale layout and alignment
 // (product_tiles.h); large MXFP4 and MXFP8 / MXFP6 problems go to the 256-row
 // pipelines (launch_linear).
-//  * k_linear_few: 32 rows by 32 columns per workgroup of 8 or 2 waves, which split K.
-//    For few rows, where reading the weight once with as many loads in flight as
+//  * k_linear_rows16: 16 rows by 16 columns per workgroup of 8, 4 or 2 waves, which
+//    split K.  For few rows, where reading the weight once with as many loads in flight as
 //    possible is all that counts.
-//    One row of N = K = 2880 5.2 us (9.0 with the call): the launch, two trips along K and
-//    one to the output for 4.2 MB.
 //  * k_linear_tile: 128 rows by 128 columns per workgroup of 8 waves, operands
 //    staged through a ring in LDS.  1037 x 1451 x 2912 MXFP8 backward 21.4 us: 108
 //    workgroups of 23 stages, 0.6 us each, on 256 CUs.
@@ -22,10 +20,144 @@ namespace mx {
 
 namespace {
 
+// ---------------------------------------------------------------- 16 x 16 tiles
+// V_MFMA_SCALE_F32_16X16X128_F8F6F4: lane l holds row (or column) l % 16 and, g = l / 16,
+// K-block g of a 128-deep piece (FP8: bytes [16 g, +16) of its first and of its second
+// half) with that block's scale.  Straight loads of that would take 16 bytes from 16 rows
+// for every 16 neighbouring lanes, one address at a time.  Instead the four lanes 4 r ..
+// 4 r + 3 load the four blocks of row r, 64 to 128 neighbouring bytes, and the words change
+// lanes in registers (ds_bpermute): 16 rows of 11264 x 4096 MXFP4 11.3 -> 8.4 us, 32 rows
+// 17.7 -> 12.1.  A wave has BD pieces of 16 columns in flight, 256 to 512 neighbouring bytes
+// of each; 32 columns by half as many bytes (32X32X64) used half of the CUs for one row.
+//
+// One row of N = K = 2880 4.4 us (MXFP8 5.9; 5.4 and 7.7 with 32 x 32 tiles): the launch, one
+// trip to memory along K and one for the epilogue.  1 x 65536 x 2880 (101 MB) 20.5 (5 TB/s),
+// 64 rows over 32 experts (142 MB) 27.2 (5.2 TB/s; MXFP8 41.5): HBM bandwidth.  us of 8, 4
+// and 2 waves: 1 x 2880 x 2880 4.4, 4.8, 6.0; 64 rows 8.9, 6.7, 8.3; 128 rows 12.8, 10.6,
+// 9.5; 64 rows over 32 experts 46, 29.4, 27.2.
+constexpr int BD = 4;                     // pieces of a batch: 16 blocks, 256 to 512 bytes of a row
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef uint32_t scale_words4 __attribute__((ext_vector_type(4)));
+typedef scale_words4 loose_scales __attribute__((aligned(1)));
+
+// Pieces [d, d1) of a row, BD of them at most; blocks at nkb and beyond as zero codes at
+// scale 1.
+template <int F>
+struct Batch {
+  static constexpr int W = elem_bits<F>();
+  uint32_t w[BD][W];
+  scale_words4 sc;                        // byte g of word i: block g of piece i
+
+  __device__ __forceinline__ void load(const OpRow& r, int d, int d1, int nkb, int g) {
+    const bool full = 4 * (d + BD) <= nkb;       // wave-uniform
+    if (full) {
+      sc = *reinterpret_cast<const loose_scales*>(r.scales + 4 * d);
+    } else {
+#pragma unroll
+      for (int i = 0; i < BD; ++i) {
+        const int kb = 4 * (d + i) + g;
+        sc[i] = (kb < nkb ? (uint32_t)r.scales[kb] : 127u) << (8 * g);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < BD; ++i) {
+      if (d + i >= d1) break;
+      const int kb = 4 * (d + i);
+      uint32_t* const q = w[i];
+      if constexpr (elem_bits<F>() == 8) {
+        uint4 x = make_uint4(0, 0, 0, 0), y = x;
+        const uint8_t* const c = r.codes + 32 * (int64_t)kb + 16 * g;
+        if (full || kb + (g >> 1) < nkb) x = *reinterpret_cast<const uint4*>(c);
+        if (full || kb + 2 + (g >> 1) < nkb) y = *reinterpret_cast<const uint4*>(c + 64);
+        q[0] = x.x, q[1] = x.y, q[2] = x.z, q[3] = x.w;
+        q[4] = y.x, q[5] = y.y, q[6] = y.z, q[7] = y.w;
+      } else if constexpr (elem_bits<F>() == 6) {
+        uint2 x = make_uint2(0, 0), y = x, z = x;
+        if (full || kb + g < nkb) {
+          const uint2* const c = reinterpret_cast<const uint2*>(r.codes + 24 * (int64_t)(kb + g));
+          x = c[0], y = c[1], z = c[2];
+        }
+        q[0] = x.x, q[1] = x.y, q[2] = y.x, q[3] = y.y, q[4] = z.x, q[5] = z.y;
+      } else {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (full || kb + g < nkb) x = *reinterpret_cast<const uint4*>(r.codes + 16 * (int64_t)(kb + g));
+        q[0] = x.x, q[1] = x.y, q[2] = x.z, q[3] = x.w;
+      }
+    }
+  }
+  // Byte i: the scale of the block that this lane multiplies of piece i.
+  __device__ __forceinline__ int scales(int g, int from) const {
+    const uint32_t pick = 0x0400u + 0x0101u * g;
+    const uint32_t lo = __builtin_amdgcn_perm(sc[1], sc[0], pick), hi = __builtin_amdgcn_perm(sc[3], sc[2], pick);
+    return __builtin_amdgcn_ds_bpermute(from, (int)__builtin_amdgcn_perm(hi, lo, 0x05040100u));
+  }
+  template <int I>
+  __device__ __forceinline__ v8i piece(int from) const {
+    v8i v = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < W; ++k) v[k] = __builtin_amdgcn_ds_bpermute(from, (int)w[I][k]);
+    return v;
+  }
+};
+
+template <int FA, int FB, int I>
+__device__ __forceinline__ v4f mul_at(const Batch<FA>& a, const Batch<FB>& b, int sa, int sb, int from, v4f acc) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.template piece<I>(from), b.template piece<I>(from), acc,
+                                                          mfma_fmt<FA>(), mfma_fmt<FB>(), I, sa, I, sb);
+}
+
 template <int FA, int FB, int FW>
-__global__ __launch_bounds__(64 * FW) void k_linear_few(GatedArgs a, GateP p, int64_t tiles, int64_t tiles_n,
-                                                        int a_words, int b_words) {
-  few_rows<true, FA, FB, FW>(a, p, tiles, tiles_n, a_words, b_words);
+__global__ __launch_bounds__(64 * FW) void k_linear_rows16(GatedArgs a, GateP p, int64_t tiles, int64_t tiles_n) {
+  __shared__ float red[FW][16][17];
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int64_t slot = t / tiles_n, n0 = (t - slot * tiles_n) * 16;
+    if (n0 >= a.N) continue;                          // (columns are padded to 8 tiles)
+    int ex, rows;
+    int64_t row0;
+    if (!place_slot<16>(a, slot, ex, row0, rows)) return;   // past the last tile
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // where this lane loads, where it multiplies and the lane that loads that
+    const int rl = lane >> 2, gl = lane & 3, l16 = lane & 15, g = lane >> 4, from = 4 * (4 * l16 + g);
+    // rows and columns past the end read the last one; their results are dropped
+    const OpRow ra = op_row(a.A, a.a_2d, row0 + (rl < rows ? rl : rows - 1));
+    MxOperand B = a.B;
+    B.codes += ex * a.stride_codes;
+    B.scales += ex * a.stride_scales;
+    const OpRow rb = op_row(B, a.b_2d, n0 + rl < a.N ? n0 + rl : a.N - 1);
+    const int nkb = (int)(a.K / 32), pieces = (nkb + 3) / 4, per = (pieces + FW - 1) / FW;
+    const int d0 = w * per, d1 = d0 + per < pieces ? d0 + per : pieces;
+    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    // this thread's bias, and its first pass's residual, come while the products run
+    const int col = threadIdx.x & 15, first = threadIdx.x >> 4;
+    float bias = 0.0f, r_first = 0.0f;
+    if (n0 + col < a.N) {
+      bias = linear_bias(a, ex, n0 + col);
+      if (a.dH && first < rows) r_first = load_out(a.dH, a.dh_bf16, (row0 + first) * a.lddh + n0 + col);
+    }
+    for (int d = d0; d < d1; d += BD) {
+      Batch<FA> ba;
+      Batch<FB> bb;
+      bb.load(rb, d, d1, nkb, gl);
+      ba.load(ra, d, d1, nkb, gl);
+      const int sa = ba.scales(gl, from), sb = bb.scales(gl, from);
+      acc = mul_at<FA, FB, 0>(ba, bb, sa, sb, from, acc);
+      if (d + 1 < d1) acc = mul_at<FA, FB, 1>(ba, bb, sa, sb, from, acc);
+      if (d + 2 < d1) acc = mul_at<FA, FB, 2>(ba, bb, sa, sb, from, acc);
+      if (d + 3 < d1) acc = mul_at<FA, FB, 3>(ba, bb, sa, sb, from, acc);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) red[w][4 * g + r][l16] = acc[r];
+    __syncthreads();
+#pragma unroll 1
+    for (int row = first; row < rows && n0 + col < a.N; row += 4 * FW) {
+      float x = red[0][row][col];
+#pragma unroll
+      for (int i = 1; i < FW; ++i) x = x + red[i][row][col];
+      const float r = row == first || !a.dH ? r_first : load_out(a.dH, a.dh_bf16, (row0 + row) * a.lddh + n0 + col);
+      store_out(a.out, a.out_bf16, (row0 + row) * a.ldo + n0 + col, linear_out(a, p, x + bias, r));
+    }
+    __syncthreads();                  // red is free again
+  }
 }
 
 template <int FA, int FB>
@@ -34,19 +166,21 @@ __global__ __launch_bounds__(512) void k_linear_tile(GatedArgs a, GateP p, int64
   row_tiles<true, FA, FB>(a, p, tiles, tiles_n, a_words, b_words);
 }
 
+template <int FA, int FB, int FW>
+void launch_rows16(const GatedArgs& a, const GateP& p, int64_t tiles, int64_t tiles_n, hipStream_t st) {
+  hipLaunchKernelGGL((k_linear_rows16<FA, FB, FW>), dim3(tile_grid(tiles)), dim3(64 * FW), 0, st, a, p, tiles, tiles_n);
+}
+
 template <int FA, int FB>
 hipError_t launch_direct(const GatedArgs& a, bool few, hipStream_t st) {
   const GateP p = gate_params(a.act, a.alpha, a.limit, a.up_shift);
-  const Words w = scale_words(a);
   if (few || !row_tiles_fit<true>(a)) {
-    const int64_t tiles_n = column_tiles(a, 32), tiles = tiles_n * slot_bound(a, 32);
-    if (2 * tiles <= 5 * (int64_t)cu_count())
-      hipLaunchKernelGGL((k_linear_few<FA, FB, 8>), dim3(tile_grid(tiles)), dim3(512), 0, st, a, p, tiles, tiles_n, w.a,
-                         w.b);
-    else
-      hipLaunchKernelGGL((k_linear_few<FA, FB, 2>), dim3(tile_grid(tiles)), dim3(128), 0, st, a, p, tiles, tiles_n, w.a,
-                         w.b);
+    const int64_t tiles_n = column_tiles(a, 16), tiles = tiles_n * slot_bound(a, 16), cus = cu_count();
+    if (tiles <= 2 * cus) launch_rows16<FA, FB, 8>(a, p, tiles, tiles_n, st);
+    else if (tiles <= 5 * cus) launch_rows16<FA, FB, 4>(a, p, tiles, tiles_n, st);
+    else launch_rows16<FA, FB, 2>(a, p, tiles, tiles_n, st);
   } else {
+    const Words w = scale_words(a);
     const int64_t tiles_n = column_tiles(a, 128), tiles = tiles_n * slot_bound(a, 128);
     hipLaunchKernelGGL((k_linear_tile<FA, FB>), dim3(tile_grid(tiles)), dim3(512), 0, st, a, p, tiles, tiles_n, w.a,
                        w.b);
@@ -67,28 +201,31 @@ hipError_t launch_direct_b(const GatedArgs& a, bool few, hipStream_t st) {
 
 }  // namespace
 
-// Which kernel (us as k_linear_few / k_linear_tile / pipeline, N = K = 2880 unless said,
+// Which kernel (us as k_linear_rows16 / k_linear_tile / pipeline, N = K = 2880 unless said,
 // bias and residual, graph replays; MXFP4, then MXFP8):
-//  * k_linear_few while its workgroups are at most 2 per CU: 1 row 5.1 / 13.2 / 25 (7.2 /
-//    17.7 / 51), 128 rows 11.7 / 13.4 (17.6 / 19.6), 128 of 4096 x 4096 15.5 / 19.8 (23.3 /
-//    25.9); 192 rows 16.9 / 13.9 (24.1 / 19.2), 64 of 11264 x 4096 25.9 / 18.2 (37.6 /
-//    23.9).  Grouped over 32 experts 16 rows 16.0 / 16.7 (27.1 / 22.7), 64 rows 41.3 / 41.5
-//    (65 / 57), 256 rows 59 / 50 (90 / 69).
+//  * k_linear_rows16 for one row tile, and while its workgroups are at most 8 per CU: 1 row of
+//    65536 20.5 / 32.2 (39 / 51), 32 rows 38 / 28 (78 / 48); 160 rows 11.3 / 14.3 (16.8 / 18.6),
+//    192 12.8 / 14.4 (18.9 / 18.9), 256 16.1 / 14.9 (22.8 / 19.0); 64 of 11264 x 4096 18.7 /
+//    17.2 (32.7 / 27.4); 512 of 1024 x 4096 13.2 / 17.8 (20.7 / 23.6).  Grouped also up to 16
+//    rows per expert, 12 of an 8-bit weight, whose bytes count for more where experts have
+//    two row tiles: over 32 experts 64 rows 27.2 / 42.9 (41.5 / 61.3), 256 rows 40.7 / 54
+//    (63 / 78), 512 rows 47 / 49.5 (77 / 69), 1024 rows 63.5 / 54.8; over 128 of 1024 x 2048
+//    2048 rows 46.9 / 57.6 (75.8 / 79); over 8 of 4096 x 4096 128 rows 25.0 / 22.1 (41 / 39).
 //  * k_linear_tile while one workgroup per CU does in MXFP4, two with wider elements: 1280
-//    rows 19.5 / 28.0, 1400 33.1 / 28.3; 2048 rows (39.7 / 55.2), 3000 (58.5 / 56.0).  Grouped
-//    in MXFP4 up to 16 rows per expert (32 experts: 512 rows 53.4 / 57.5, 768 63.8 / 58.3; 128
-//    of 1024 x 2048: 1024 rows 50 / 46, 8192 73 / 64) or 5 workgroups per 4 CUs (8 of 4096 x
-//    4096: 256 rows 21.3 / 30.7, 1024 39 / 32), up to 128 with wider elements (32 experts:
-//    2048 rows 94 / 114, 4096 119 / 118, 8192 180 / 167; 8 of 4096 x 4096: 1024 69 / 85,
-//    4096 159 / 151).  Also everything that the pipelines do not take.
+//    rows 19.5 / 28.0 (tile, pipeline), 1400 33.1 / 28.3; 2048 rows (39.7 / 55.2),
+//    3000 (58.5 / 56.0).  Grouped in MXFP4 up to 5 workgroups per 4 CUs (8 of 4096 x 4096: 256
+//    rows 21.3 / 30.7, 1024 39 / 32; 32 experts: 768 rows 63.8 / 58.3), up to 128 rows per
+//    expert with wider elements (32 experts: 2048 rows 94 / 114, 4096 119 / 118, 8192 180 /
+//    167; 8 of 4096 x 4096: 1024 69 / 85, 4096 159 / 151).  Also everything that the pipelines
+//    do not take.
 //  * the 256-row pipelines beyond.
 hipError_t launch_linear(const GatedArgs& a, hipStream_t st) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
   const int64_t cus = cu_count();
-  const int64_t few_wgs = (a.N + 31) / 32 * slot_bound(a, 32), tile_wgs = column_tiles(a, 128) * slot_bound(a, 128);
-  const bool f4 = a.a_elem == 0 && a.b_elem == 0;
-  const bool few = few_wgs <= 2 * cus;
-  const bool tile = a.offsets ? a.M <= (f4 ? 16 : 128) * (int64_t)a.E || (f4 && 4 * tile_wgs <= 5 * cus)
+  const int64_t few_wgs = column_tiles(a, 16) * slot_bound(a, 16), tile_wgs = column_tiles(a, 128) * slot_bound(a, 128);
+  const bool f4 = a.a_elem == 0 && a.b_elem == 0, wide = a.b_elem == 1 || a.b_elem == 2;
+  const bool few = few_wgs <= 8 * cus || (a.offsets ? a.M <= (wide ? 12 : 16) * (int64_t)a.E : a.M <= 16);
+  const bool tile = a.offsets ? (f4 ? 4 * tile_wgs <= 5 * cus : a.M <= 128 * (int64_t)a.E)
                               : tile_wgs <= (f4 ? 1 : 2) * cus;
   if (!few && !tile) {
     if (linear256_layout_ok(a)) return launch_linear256(a, st);
