@@ -32,8 +32,9 @@ namespace {
 //
 // One row of N = K = 2880 4.4 us (MXFP8 5.9; 5.4 and 7.7 with 32 x 32 tiles): the launch, one
 // trip to memory along K and one for the epilogue.  1 x 65536 x 2880 (101 MB) 20.5 (5 TB/s),
-// 64 rows over 32 experts (142 MB) 27.2 (5.2 TB/s; MXFP8 41.5): HBM bandwidth.  us of 8, 4
-// and 2 waves: 1 x 2880 x 2880 4.4, 4.8, 6.0; 64 rows 8.9, 6.7, 8.3; 128 rows 12.8, 10.6,
+// 64 rows over 32 experts, 22 of them with rows, 27-29 (97 MB; MXFP8 42-48, 188 MB): HBM
+// bandwidth, and two trips to memory before the first weights arrive.  us of 8, 4 and 2
+// waves: 1 x 2880 x 2880 4.4, 4.8, 6.0; 64 rows 8.9, 6.7, 8.3; 128 rows 12.8, 10.6,
 // 9.5; 64 rows over 32 experts 46, 29.4, 27.2.
 constexpr int BD = 4;                     // pieces of a batch: 16 blocks, 256 to 512 bytes of a row
 typedef float v4f __attribute__((ext_vector_type(4)));
