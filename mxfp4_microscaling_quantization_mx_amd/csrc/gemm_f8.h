@@ -228,6 +228,12 @@ __device__ __forceinline__ void f8_compute(v16f acc[2][4], uint32_t slot, uint32
   }
 }
 
+// A value that every lane of the wave holds alike, in scalar registers.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32 | (uint32_t)uniform((int)x));
+}
+
 // Persistent: one workgroup per CU walks its list of tiles (Sched: the dense
 // XCD-contiguous ranges in groups of 8 M-tiles, or the grouped GEMM's expert
 // row tiles), and the stage sequence runs on across tiles: the next tile's
@@ -264,7 +270,7 @@ __device__ __forceinline__ void run_f8(const Sched& sc, const MxOperand& A, cons
   const int64_t lds_s = sA ? A.ld_scales : B.ld_scales;
   // Tile j of this workgroup: the lane's load state, and the tile's output
   // origin (row of C, column) and extent.
-  auto setup = [&](int j, F8Lane& L, int64_t& crow0, int& n0, int& mlim, int& nlim, int& ex) {
+  auto setup = [&](int j, F8Lane& L, int64_t& crow0, int& n0, int& mlim, int& nlim) {
     const t256::TileInfo ti = sc.tile(j);
     mlim = ti.M - ti.m0;
     nlim = ti.N - ti.n0;
@@ -298,14 +304,13 @@ __device__ __forceinline__ void run_f8(const Sched& sc, const MxOperand& A, cons
     L.so = sr >= 0 ? (uint32_t)((s2d ? (sr >> 5) : sr) * lds_s) : MX_OOB;
     crow0 = ti.c_row0;
     n0 = ti.n0;
-    if constexpr (LINEAR) ex = ti.ex;
   };
   const int nst = (K + 127) / 128;
   const uint32_t a_slots = (uint32_t)(uintptr_t)(f8::lds_t)slots, a_sws = (uint32_t)(uintptr_t)(f8::lds_t)sws;
   F8Lane L;
   int64_t c0 = 0, c0n = 0;
-  int n0 = 0, mlim = 0, nlim = 0, ex = 0, n0n = 0, mln = 0, nln = 0, exn = 0;
-  if (ntiles > 0) setup(0, L, c0, n0, mlim, nlim, ex);
+  int n0 = 0, mlim = 0, nlim = 0, n0n = 0, mln = 0, nln = 0;
+  if (ntiles > 0) setup(0, L, c0, n0, mlim, nlim);
   if (ntiles > 0 && nst > 0) f8_issue<FA, FB>(L, 0, K, slots, sws, wave);
   int g = 0;                                                  // stages multiplied so far (slot g & 1)
   for (int j = 0; j < ntiles; ++j) {
@@ -325,7 +330,7 @@ __device__ __forceinline__ void run_f8(const Sched& sc, const MxOperand& A, cons
         f8_issue<FA, FB>(L, s + 1, K, slots + nx * f8::SLOT, sws + nx * f8::SWORDS, wave);
       } else if (j + 1 < ntiles) {
         // tile j issues nothing more: its load state becomes tile j + 1's
-        setup(j + 1, L, c0n, n0n, mln, nln, exn);
+        setup(j + 1, L, c0n, n0n, mln, nln);
         f8_issue<FA, FB>(L, 0, K, slots + nx * f8::SLOT, sws + nx * f8::SWORDS, wave);
       }
       f8_compute<FA, FB, SWAP>(acc.t, a_slots + (uint32_t)((g & 1) * f8::SLOT),
@@ -349,18 +354,23 @@ __device__ __forceinline__ void run_f8(const Sched& sc, const MxOperand& A, cons
         t256::store_tile_gate<false, t256c::B_INTERLEAVED>(acc, q, c0, n0, mlim, nlim);
       }
     } else if constexpr (LINEAR) {
-      t256::store_tile_linear<t256::ACT_ANY, OUT == 5>(acc, t256c::load_gate_out(lo), c0, n0, mlim, nlim, ex, 0u);
+      // The tile's place is the same in every lane, which this says: without it the compiler
+      // takes each buffer for one per lane and puts every load and store in a loop over
+      // them.  The expert is looked up again: one more value kept with the place cost the
+      // other epilogues theirs (loops in k_gemm_f8, 268 -> 277 us at 16384 x 5760 x 2880 MXFP8,
+      // and spills in k_gemm_f8_q).
+      t256::store_tile_linear<t256::ACT_ANY, OUT == 5>(acc, t256c::load_gate_out(lo), uniform(c0), uniform(n0),
+                                                       uniform(mlim), uniform(nlim), uniform(sc.tile(j).ex), 0u);
     } else {
       constexpr int ES = OUT_BF16 ? 2 : 4;
       t256::store_tile<OUT_BF16>(acc, static_cast<uint8_t*>(C) + (c0 * ldc + n0) * ES, (int)ldc, mlim, nlim);
     }
     if (j + 1 < ntiles) {
-      if (nst == 0) setup(j + 1, L, c0n, n0n, mln, nln, exn);
+      if (nst == 0) setup(j + 1, L, c0n, n0n, mln, nln);
       c0 = c0n;
       n0 = n0n;
       mlim = mln;
       nlim = nln;
-      ex = exn;
     }
   }
 }
