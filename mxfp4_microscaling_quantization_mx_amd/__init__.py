@@ -54,6 +54,7 @@ _ELEM = {"e2m1": (0, 4), "e4m3": (1, 8), "e5m2": (2, 8), "e2m3": (3, 6), "e3m2":
 _ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 _EPILOGUE_ACT = {**_ACT, None: 3}
 _SCORE = {"softmax": 0, "sigmoid": 1}
+_EXPERTS_MAX, _CHOICES_MAX = 1024, 64           # of a router (mx_route in include/mx.h)
 _GATE_LAYOUT = {"interleaved": 0, "halves": 1}
 _DTYPE = {torch.float32: MX_DT_F32, torch.bfloat16: MX_DT_BF16}
 
@@ -730,6 +731,13 @@ def _slots(t, what, dtype, shape=None):
         raise ValueError(f"{what} must have shape {tuple(shape)}")
 
 
+def _size(n, most):
+    """A size as the library is told it, and as its outputs are allocated: the library
+    turns down what is outside [0, most] before it looks at a buffer, so such a size
+    allocates no more than that."""
+    return max(-1, min(n, most + 1)), max(0, min(n, most))
+
+
 def route(logits, top, router=Router()):
     """The `top` experts of every token and their weights from the logits
     [T, E], bf16 or float32 (see mx_route): (ids int32 [T, top], weights
@@ -738,8 +746,9 @@ def route(logits, top, router=Router()):
     ld = _check_rows(logits, "route: logits")
     st = _stream(logits)
     T, E = logits.shape
-    ids = logits.new_empty((T, top), dtype=torch.int32)
-    weights = logits.new_empty((T, top), dtype=torch.float32)
+    top, n = _size(top, _CHOICES_MAX)
+    ids = logits.new_empty((T, n), dtype=torch.int32)
+    weights = logits.new_empty((T, n), dtype=torch.float32)
     cfg = router.c_struct()
     _check(lib.mx_route(_ptr(logits), _DTYPE[logits.dtype], T, E, ld, top, ctypes.byref(cfg), _ptr(ids),
                         _ptr(weights), st))
@@ -777,8 +786,8 @@ def expert_sort(ids, E):
     _slots(ids, "expert_sort: ids", torch.int32)
     st = _stream(ids)
     T, top = ids.shape
-    # (E may be refused: the library answers before it looks at the buffers)
-    offsets, rows, dest = ids.new_empty(max(E, 0) + 1), ids.new_empty(T * top), ids.new_empty((T, top))
+    E, n = _size(E, _EXPERTS_MAX)
+    offsets, rows, dest = ids.new_empty(n + 1), ids.new_empty(T * top), ids.new_empty((T, top))
     nbytes = _sort_workspace(T, top, E)
     ws = ids.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
     _check(lib.mx_expert_sort(_ptr(ids), T, top, E, _ptr(offsets), _ptr(rows), _ptr(dest), _ptr(ws), nbytes, st))
