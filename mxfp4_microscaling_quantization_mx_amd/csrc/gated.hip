@@ -186,7 +186,7 @@ hipError_t launch_direct(const GatedArgs& a, bool few, hipStream_t st) {
   const GateP p = gate_params(a.act, a.alpha, a.limit, a.up_shift);
   const int a_words = scale_words(a).a, b_words = scale_words(a).b;
   if (few || !row_tiles_fit<false>(a)) {
-    const int64_t tiles_n = column_tiles(a, 16), tiles = tiles_n * slot_bound(a, 32);
+    const int64_t tiles_n = column_tiles(a.M, a.N, 16), tiles = tiles_n * slot_bound(a, 32);
     if (2 * tiles <= 5 * (int64_t)cu_count())
       hipLaunchKernelGGL((k_gated_few<FA, FB, 8>), dim3(tile_grid(tiles)), dim3(512), 0, st, a, p, tiles, tiles_n,
                          a_words, b_words);
@@ -194,7 +194,7 @@ hipError_t launch_direct(const GatedArgs& a, bool few, hipStream_t st) {
       hipLaunchKernelGGL((k_gated_few<FA, FB, 2>), dim3(tile_grid(tiles)), dim3(128), 0, st, a, p, tiles, tiles_n,
                          a_words, b_words);
   } else {
-    const int64_t tiles_n = column_tiles(a, 64), tiles = tiles_n * slot_bound(a, 128);
+    const int64_t tiles_n = column_tiles(a.M, a.N, 64), tiles = tiles_n * slot_bound(a, 128);
     hipLaunchKernelGGL((k_gated_tile<FA, FB>), dim3(tile_grid(tiles)), dim3(512), 0, st, a, p, tiles, tiles_n, a_words,
                        b_words);
   }

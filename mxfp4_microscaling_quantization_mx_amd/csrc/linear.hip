@@ -176,13 +176,13 @@ template <int FA, int FB>
 hipError_t launch_direct(const GatedArgs& a, bool few, hipStream_t st) {
   const GateP p = gate_params(a.act, a.alpha, a.limit, a.up_shift);
   if (few || !row_tiles_fit<true>(a)) {
-    const int64_t tiles_n = column_tiles(a, 16), tiles = tiles_n * slot_bound(a, 16), cus = cu_count();
+    const int64_t tiles_n = column_tiles(a.M, a.N, 16), tiles = tiles_n * slot_bound(a, 16), cus = cu_count();
     if (tiles <= 2 * cus) launch_rows16<FA, FB, 8>(a, p, tiles, tiles_n, st);
     else if (tiles <= 5 * cus) launch_rows16<FA, FB, 4>(a, p, tiles, tiles_n, st);
     else launch_rows16<FA, FB, 2>(a, p, tiles, tiles_n, st);
   } else {
     const Words w = scale_words(a);
-    const int64_t tiles_n = column_tiles(a, 128), tiles = tiles_n * slot_bound(a, 128);
+    const int64_t tiles_n = column_tiles(a.M, a.N, 128), tiles = tiles_n * slot_bound(a, 128);
     hipLaunchKernelGGL((k_linear_tile<FA, FB>), dim3(tile_grid(tiles)), dim3(512), 0, st, a, p, tiles, tiles_n, w.a,
                        w.b);
   }
@@ -223,7 +223,7 @@ hipError_t launch_direct_b(const GatedArgs& a, bool few, hipStream_t st) {
 hipError_t launch_linear(const GatedArgs& a, hipStream_t st) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
   const int64_t cus = cu_count();
-  const int64_t few_wgs = column_tiles(a, 16) * slot_bound(a, 16), tile_wgs = column_tiles(a, 128) * slot_bound(a, 128);
+  const int64_t few_wgs = column_tiles(a.M, a.N, 16) * slot_bound(a, 16), tile_wgs = column_tiles(a.M, a.N, 128) * slot_bound(a, 128);
   const bool f4 = a.a_elem == 0 && a.b_elem == 0, wide = a.b_elem == 1 || a.b_elem == 2;
   const bool few = few_wgs <= 8 * cus || (a.offsets ? a.M <= (wide ? 12 : 16) * (int64_t)a.E : a.M <= 16);
   const bool tile = a.offsets ? (f4 ? 4 * tile_wgs <= 5 * cus : a.M <= 128 * (int64_t)a.E)

@@ -10,6 +10,7 @@
 
 #include "gate_device.h"
 #include "group_device.h"
+#include "launch_rule.h"
 #include "mx_device.h"
 #include "mx_launch.h"
 
@@ -455,14 +456,6 @@ __device__ __forceinline__ void row_tiles(const GatedArgs& a, const GateP& p, in
 int64_t slot_bound(const GatedArgs& a, int TM) {
   if (!a.offsets) return (a.M + TM - 1) / TM;
   return a.M / TM + (a.E < a.M ? a.E : a.M);
-}
-
-// Column tiles per row tile, padded to a multiple of 8 where there are several
-// row tiles: a column tile's workgroups then run on one XCD (workgroup b on
-// XCD b % 8) and share its weight rows in one L2.
-int64_t column_tiles(const GatedArgs& a, int TN) {
-  const int64_t n = (a.N + TN - 1) / TN;
-  return a.M > 32 ? (n + 7) / 8 * 8 : n;
 }
 
 unsigned tile_grid(int64_t tiles) { return (unsigned)(tiles < (1 << 20) ? tiles : (1 << 20)); }
