@@ -33,9 +33,7 @@ namespace {
 // One row of N = K = 2880 4.4 us (MXFP8 5.9; 5.4 and 7.7 with 32 x 32 tiles): the launch, one
 // trip to memory along K and one for the epilogue.  1 x 65536 x 2880 (101 MB) 20.5 (5 TB/s),
 // 64 rows over 32 experts, 22 of them with rows, 27-29 (97 MB; MXFP8 42-48, 188 MB): HBM
-// bandwidth, and two trips to memory before the first weights arrive.  us of 8, 4 and 2
-// waves: 1 x 2880 x 2880 4.4, 4.8, 6.0; 64 rows 8.9, 6.7, 8.3; 128 rows 12.8, 10.6,
-// 9.5; 64 rows over 32 experts 46, 29.4, 27.2.
+// bandwidth, and two trips to memory before the first weights arrive.
 constexpr int BD = 4;                     // pieces of a batch: 16 blocks, 256 to 512 bytes of a row
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t scale_words4 __attribute__((ext_vector_type(4)));
@@ -176,9 +174,10 @@ template <int FA, int FB>
 hipError_t launch_direct(const GatedArgs& a, bool few, hipStream_t st) {
   const GateP p = gate_params(a.act, a.alpha, a.limit, a.up_shift);
   if (few || !row_tiles_fit<true>(a)) {
-    const int64_t tiles_n = column_tiles(a.M, a.N, 16), tiles = tiles_n * slot_bound(a, 16), cus = cu_count();
-    if (tiles <= 2 * cus) launch_rows16<FA, FB, 8>(a, p, tiles, tiles_n, st);
-    else if (tiles <= 5 * cus) launch_rows16<FA, FB, 4>(a, p, tiles, tiles_n, st);
+    const int64_t tiles_n = column_tiles(a.M, a.N, 16), tiles = tiles_n * slot_bound(a, 16);
+    const int waves = rows16_waves(a.M, a.N, a.offsets ? a.E : 0, cu_count());
+    if (waves == 8) launch_rows16<FA, FB, 8>(a, p, tiles, tiles_n, st);
+    else if (waves == 4) launch_rows16<FA, FB, 4>(a, p, tiles, tiles_n, st);
     else launch_rows16<FA, FB, 2>(a, p, tiles, tiles_n, st);
   } else {
     const Words w = scale_words(a);
@@ -202,33 +201,13 @@ hipError_t launch_direct_b(const GatedArgs& a, bool few, hipStream_t st) {
 
 }  // namespace
 
-// Which kernel (us as k_linear_rows16 / k_linear_tile / pipeline, N = K = 2880 unless said,
-// bias and residual, graph replays; MXFP4, then MXFP8):
-//  * k_linear_rows16 for one row tile, and while its workgroups are at most 8 per CU: 1 row of
-//    65536 20.5 / 32.2 (39 / 51), 32 rows 38 / 28 (78 / 48); 160 rows 11.3 / 14.3 (16.8 / 18.6),
-//    192 12.8 / 14.4 (18.9 / 18.9), 256 16.1 / 14.9 (22.8 / 19.0); 64 of 11264 x 4096 18.7 /
-//    17.2 (32.7 / 27.4); 512 of 1024 x 4096 13.2 / 17.8 (20.7 / 23.6).  Grouped also up to 16
-//    rows per expert, 12 of an 8-bit weight, whose bytes count for more where experts have
-//    two row tiles: over 32 experts 64 rows 27.2 / 42.9 (41.5 / 61.3), 256 rows 40.7 / 54
-//    (63 / 78), 512 rows 47 / 49.5 (77 / 69), 1024 rows 63.5 / 54.8; over 128 of 1024 x 2048
-//    2048 rows 46.9 / 57.6 (75.8 / 79); over 8 of 4096 x 4096 128 rows 25.0 / 22.1 (41 / 39).
-//  * k_linear_tile while one workgroup per CU does in MXFP4, two with wider elements: 1280
-//    rows 19.5 / 28.0 (tile, pipeline), 1400 33.1 / 28.3; 2048 rows (39.7 / 55.2),
-//    3000 (58.5 / 56.0).  Grouped in MXFP4 up to 5 workgroups per 4 CUs (8 of 4096 x 4096: 256
-//    rows 21.3 / 30.7, 1024 39 / 32; 32 experts: 768 rows 63.8 / 58.3), up to 128 rows per
-//    expert with wider elements (32 experts: 2048 rows 94 / 114, 4096 119 / 118, 8192 180 /
-//    167; 8 of 4096 x 4096: 1024 69 / 85, 4096 159 / 151).  Also everything that the pipelines
-//    do not take.
-//  * the 256-row pipelines beyond.
+// (the rule and what it was measured by: launch_rule.h)
 hipError_t launch_linear(const GatedArgs& a, hipStream_t st) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
-  const int64_t cus = cu_count();
-  const int64_t few_wgs = column_tiles(a.M, a.N, 16) * slot_bound(a, 16), tile_wgs = column_tiles(a.M, a.N, 128) * slot_bound(a, 128);
-  const bool f4 = a.a_elem == 0 && a.b_elem == 0, wide = a.b_elem == 1 || a.b_elem == 2;
-  const bool few = few_wgs <= 8 * cus || (a.offsets ? a.M <= (wide ? 12 : 16) * (int64_t)a.E : a.M <= 16);
-  const bool tile = a.offsets ? (f4 ? 4 * tile_wgs <= 5 * cus : a.M <= 128 * (int64_t)a.E)
-                              : tile_wgs <= (f4 ? 1 : 2) * cus;
-  if (!few && !tile) {
+  const LinearKernel kernel = linear_kernel(a.M, a.N, a.offsets ? a.E : 0, a.a_elem == 0 && a.b_elem == 0,
+                                            a.b_elem == 1 || a.b_elem == 2, cu_count());
+  const bool few = kernel == LinearKernel::ROWS16;
+  if (kernel == LinearKernel::PIPELINE) {
     if (linear256_layout_ok(a)) return launch_linear256(a, st);
     if (linear_f8_layout_ok(a)) return launch_linear_f8(a, st);
   }

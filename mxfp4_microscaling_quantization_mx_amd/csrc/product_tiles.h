@@ -451,12 +451,7 @@ __device__ __forceinline__ void row_tiles(const GatedArgs& a, const GateP& p, in
   }
 }
 
-// Row tiles of TM rows a grouped launch must offer: every expert with rows
-// adds at most one partial tile.
-int64_t slot_bound(const GatedArgs& a, int TM) {
-  if (!a.offsets) return (a.M + TM - 1) / TM;
-  return a.M / TM + (a.E < a.M ? a.E : a.M);
-}
+int64_t slot_bound(const GatedArgs& a, int TM) { return row_tiles_bound(a.M, a.offsets ? a.E : 0, TM); }
 
 unsigned tile_grid(int64_t tiles) { return (unsigned)(tiles < (1 << 20) ? tiles : (1 << 20)); }
 
