@@ -1213,7 +1213,7 @@ mx_status linear_args(const mx_tensor* A, const mx_tensor* B, const mx_epilogue_
     return fail(MX_ERR_INVALID_ARG, "%s: A.K=%lld != B.K=%lld", what, (long long)A->K, (long long)B->K);
   const int32_t act = cfg ? cfg->act : (int32_t)MX_ACT_NONE;
   if (act < MX_ACT_SILU || act > MX_ACT_NONE) return fail(MX_ERR_INVALID_ARG, "%s: unknown activation %d", what, act);
-  if (cfg && (!(cfg->alpha > 0.0f) || !std::isfinite(cfg->alpha)))
+  if (act == MX_ACT_SILU && (!(cfg->alpha > 0.0f) || !std::isfinite(cfg->alpha)))   // (the others ignore it)
     return fail(MX_ERR_INVALID_ARG, "%s: alpha must be finite and > 0", what);
   if (backward && act == MX_ACT_NONE)
     return fail(MX_ERR_INVALID_ARG, "%s: without an activation the gradient is dY itself", what);
@@ -1235,7 +1235,7 @@ mx_status linear_args(const mx_tensor* A, const mx_tensor* B, const mx_epilogue_
   a.N = B->rows;
   a.K = A->K;
   a.act = act;
-  a.alpha = cfg ? cfg->alpha : 1.0f;
+  a.alpha = act == MX_ACT_SILU ? cfg->alpha : 1.0f;
   a.backward = backward;
   if (a.M == 0 || a.N == 0) return MX_OK;
   st = check_rows(out.p, out.dtype, a.N, out.ld, what, backward ? "dP" : "Y");
