@@ -54,7 +54,8 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 
 // e^x for x <= 0 within 2 ulp: x log2 e in two parts, the second of which moves
-// the result by less than 2^-16 of itself.  Below 2^-126 it is 0; NaN stays.
+// the result by less than 2^-16 of itself.  Below 2^-126 it is 0, so that a weight may err
+// by that over its sum, which is 1/2 (sigmoid) or more; NaN stays.
 __device__ __forceinline__ float exp_neg(float x) {
   const float c = __builtin_elementwise_maximum(x, -200.0f);
   const float t = c * 1.44269504f;
