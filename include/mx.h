@@ -650,10 +650,10 @@ typedef struct {
  * (for softmax the softmax of the chosen logits).  Computed in float32: a weight
  * errs by at most (32 + ln E + d) 2^-24 of itself, d the distance of its logit from
  * the token's largest, or by 2^-125 |scale| where that is more (what lies below float32's
- * smallest normal number on the way may become 0).  Where the largest logit is -Inf (a token that may go
- * nowhere) the weights are 0, whatever the ids; other -Inf logits have weight 0.
- * NaN among the logits that a sum takes, or +Inf in a softmax, makes the token's
- * weights NaN; a NaN logit's own weight is NaN.
+ * smallest normal number on the way may become 0).  Where the largest logit is -Inf (a
+ * token that may go nowhere) the weights are 0, whatever the ids; other -Inf logits have
+ * weight 0.  NaN among the logits that a sum takes, or +Inf in a softmax, makes the
+ * token's weights NaN; a NaN logit's own weight is NaN.
  *
  *   logits   device; [T, E] of `dtype` (mx_dtype), row stride ld elements (>= E).
  *   E        1 .. 1024; top 1 .. min(E, 64) (above 64 or 1024: MX_ERR_UNSUPPORTED).
