@@ -9,10 +9,17 @@
 //
 // Bound by HBM bandwidth (a device copy 5.05 TB/s): 16384 x 2880 bf16, 4 choices, combine
 // 90 us without and 105-107 with a residual (478 MB read, 94 written, 5.3 TB/s), backward
-// 160-162 (5.3), dispatch 79 (6.0).  A lane has all its choices' pieces, four at a time,
-// in flight at once, which is enough beside the other waves of a CU.  Rows that start
-// at any element cost the cache lines that their pieces straddle: 16384 x 2879 bf16 109
-// us for 90, 4099 x 1111 bf16 16.1 (2.8 TB/s), float32 16.2 (5.6), backward 31 and 41.
+// 160-162 (5.3), dispatch 79 (6.0).  In wide rows a lane has the whole 16-byte pieces of its
+// choices, four at a time, in flight at once, which is enough beside the other waves of a
+// CU.  Two things do not overlap:
+//  * a row's last piece where it is not whole: its elements are loaded one at a time, in bf16
+//    each waited for before the next, up to 7 per choice.  4099 x 1111 bf16 16.0 us, at a
+//    stride of 1112 too, and 10.3 with 1112 columns; backward 31 and 17.6; 16384 x 2879 110
+//    and 91 with 2880.  In float32 (up to 3 elements) 17.7 with either, backward 41 and 34.
+//  * rows of at most 32 pieces, laid side by side: each lane reads its own entries of dest
+//    and waits for one before it requests that choice's row.  The backward pass gives every
+//    token a workgroup, whatever its width, and reads dest and weights first: 8192 x 32, 64
+//    or 128 columns 9 us.
 #include "row_device.h"
 #include "mx_launch.h"
 

@@ -7,12 +7,12 @@
 //
 // The kernels here take any shape, element types, scale layout and alignment
 // (product_tiles.h); large MXFP4 and MXFP8 / MXFP6 problems go to the 256-row
-// pipelines (launch_linear).
+// pipelines (the rule is in launch_rule.h).
 //  * k_linear_rows16: 16 rows by 16 columns per workgroup of 8, 4 or 2 waves, which
 //    split K.  For few rows, where reading the weight once with as many loads in flight as
 //    possible is all that counts.
 //  * k_linear_tile: 128 rows by 128 columns per workgroup of 8 waves, operands
-//    staged through a ring in LDS.  1037 x 1451 x 2912 MXFP8 backward 21.4 us: 108
+//    staged through a ring in LDS.  1037 x 1451 x 2912 MXFP8 backward 21.3 us: 108
 //    workgroups of 23 stages, 0.6 us each, on 256 CUs.
 #include "product_tiles.h"
 
@@ -126,7 +126,8 @@ __global__ __launch_bounds__(64 * FW) void k_linear_rows16(GatedArgs a, GateP p,
     const int nkb = (int)(a.K / 32), pieces = (nkb + 3) / 4, per = (pieces + FW - 1) / FW;
     const int d0 = w * per, d1 = d0 + per < pieces ? d0 + per : pieces;
     v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    // this thread's bias, and its first pass's residual, come while the products run
+    // this thread's bias, and its first pass's residual: float32 ones come while the products
+    // run, bf16 ones (shifted where they are loaded) are waited for here
     const int col = threadIdx.x & 15, first = threadIdx.x >> 4;
     float bias = 0.0f, r_first = 0.0f;
     if (n0 + col < a.N) {

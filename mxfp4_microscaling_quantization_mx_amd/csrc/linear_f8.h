@@ -2,8 +2,8 @@
 // operands (gemm_f8.h), any pair of E4M3, E5M2, E2M3 and E3M2: the tile order and the
 // epilogue of the MXFP4 kernels, the activation chosen at run time (the product is twice
 // as long, and 64 kernels are enough to compile).  16384 x 2880 x 2880 with bias and
-// residual: MXFP8 162 us (1.7 PFLOP/s), SiLU 161, GELU 174, its tanh form 164, backward 166 /
-// 174 / 167; MXFP6 153, 152, 164, 154, backward 157 / 164 / 157.
+// residual: MXFP8 162 us (1.7 PFLOP/s; the plain product 150), SiLU 161, GELU 174, its tanh
+// form 164, backward 166 / 174 / 167; MXFP6 153, 152, 164, 154, backward 157 / 164 / 157.
 #pragma once
 
 #define MX_T256_NS t256

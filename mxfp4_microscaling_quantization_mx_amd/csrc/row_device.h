@@ -45,7 +45,7 @@ struct RowPiece {
     return w;
   }
 
-  // n elements at p (n < VEC: the row's last ones, the rest 0).
+  // n elements at p (n < VEC: the row's last ones, one at a time, the rest 0).
   static __device__ __forceinline__ words load(const void* p, int n) {
     if (n >= VEC) return *static_cast<const loose_words*>(p);
     words w = {0u, 0u, 0u, 0u};
