@@ -218,7 +218,7 @@ __device__ __forceinline__ void build_expert_table(const int32_t* __restrict__ o
 }
 
 // The linear epilogue of a launch.
-inline t256c::LinearOut linear_out(const GatedArgs& a) {
+inline t256c::LinearOut linear_out(const LinearArgs& a) {
   return t256c::LinearOut{gate_params(a.act, a.alpha, a.limit, a.up_shift),
                           (a.out_bf16 ? t256c::LIN_OUT_BF16 : 0) | (a.dh_bf16 ? t256c::LIN_R_BF16 : 0) |
                               (a.bias_bf16 ? t256c::LIN_BIAS_BF16 : 0),

@@ -26,7 +26,12 @@ __device__ __forceinline__ bool find_slot(const int32_t* __restrict__ off, int E
   for (int base = 0; base < E; base += 64) {
     const int e = base + lane;
     int64_t l0 = 0, h0 = 0;
-    if (e < E) expert_rows(off, e, cap, l0, h0);
+    if (e < E) {                      // (expert_rows, written out: called, it cost k_gated_tile 1 %)
+      l0 = off[e];
+      h0 = off[e + 1];
+      l0 = l0 < 0 ? 0 : (l0 > cap ? cap : l0);
+      h0 = h0 < l0 ? l0 : (h0 > cap ? cap : h0);
+    }
     const int tiles = (int)((h0 - l0 + TM - 1) / TM);
     int incl = tiles;
 #pragma unroll

@@ -106,7 +106,7 @@ __device__ __forceinline__ v4f mul_at(const Batch<FA>& a, const Batch<FB>& b, in
 }
 
 template <int FA, int FB, int FW>
-__global__ __launch_bounds__(64 * FW) void k_linear_rows16(GatedArgs a, GateP p, int64_t tiles, int64_t tiles_n) {
+__global__ __launch_bounds__(64 * FW) void k_linear_rows16(LinearArgs a, GateP p, int64_t tiles, int64_t tiles_n) {
   __shared__ float red[FW][16][17];
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int64_t slot = t / tiles_n, n0 = (t - slot * tiles_n) * 16;
@@ -161,18 +161,18 @@ __global__ __launch_bounds__(64 * FW) void k_linear_rows16(GatedArgs a, GateP p,
 }
 
 template <int FA, int FB>
-__global__ __launch_bounds__(512) void k_linear_tile(GatedArgs a, GateP p, int64_t tiles, int64_t tiles_n, int a_words,
+__global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a, GateP p, int64_t tiles, int64_t tiles_n, int a_words,
                                                      int b_words) {
   row_tiles<true, FA, FB>(a, p, tiles, tiles_n, a_words, b_words);
 }
 
 template <int FA, int FB, int FW>
-void launch_rows16(const GatedArgs& a, const GateP& p, int64_t tiles, int64_t tiles_n, hipStream_t st) {
+void launch_rows16(const LinearArgs& a, const GateP& p, int64_t tiles, int64_t tiles_n, hipStream_t st) {
   hipLaunchKernelGGL((k_linear_rows16<FA, FB, FW>), dim3(tile_grid(tiles)), dim3(64 * FW), 0, st, a, p, tiles, tiles_n);
 }
 
 template <int FA, int FB>
-hipError_t launch_direct(const GatedArgs& a, bool few, hipStream_t st) {
+hipError_t launch_direct(const LinearArgs& a, bool few, hipStream_t st) {
   const GateP p = gate_params(a.act, a.alpha, a.limit, a.up_shift);
   if (few || !row_tiles_fit<true>(a)) {
     const int64_t tiles_n = column_tiles(a.M, a.N, 16), tiles = tiles_n * slot_bound(a, 16);
@@ -190,7 +190,7 @@ hipError_t launch_direct(const GatedArgs& a, bool few, hipStream_t st) {
 }
 
 template <int FA>
-hipError_t launch_direct_b(const GatedArgs& a, bool few, hipStream_t st) {
+hipError_t launch_direct_b(const LinearArgs& a, bool few, hipStream_t st) {
   switch (a.b_elem) {
     case 1: return launch_direct<FA, 1>(a, few, st);
     case 2: return launch_direct<FA, 2>(a, few, st);
@@ -203,7 +203,7 @@ hipError_t launch_direct_b(const GatedArgs& a, bool few, hipStream_t st) {
 }  // namespace
 
 // (the rule and what it was measured by: launch_rule.h)
-hipError_t launch_linear(const GatedArgs& a, hipStream_t st) {
+hipError_t launch_linear(const LinearArgs& a, hipStream_t st) {
   if (a.M == 0 || a.N == 0) return hipSuccess;
   const LinearKernel kernel = linear_kernel(a.M, a.N, a.offsets ? a.E : 0, a.a_elem == 0 && a.b_elem == 0,
                                             a.b_elem == 1 || a.b_elem == 2, cu_count());

@@ -61,7 +61,7 @@ __global__ __launch_bounds__(64 * GW, 1) void k_grouped_linear256(MxOperand A, M
 
 // OUT: an output kind of run_tiles.
 template <bool A2D, bool B2D, int OUT>
-hipError_t launch_out(const GatedArgs& a, hipStream_t st) {
+hipError_t launch_out(const LinearArgs& a, hipStream_t st) {
   const int cus = cu_count();
   const int tiles_n = (int)((a.N + 255) / 256);
   const int64_t tiles_m = a.offsets ? (a.M + 255) / 256 + a.E : (a.M + 255) / 256;

@@ -8,7 +8,7 @@ namespace mx {
 // and a tile's rows of the buffers, with 32-bit offsets.  The kernels with an activation
 // take 1-D scales of A only: one more layout would double them for a case (2-D scales
 // are for weights) that the 128-row tiles serve.
-bool linear256_layout_ok(const GatedArgs& a) {
+bool linear256_layout_ok(const LinearArgs& a) {
   const int64_t lim = 1ll << 31;
   const bool words = a.A.ld_scales % 16 == 0 && a.B.ld_scales % 16 == 0 && a.stride_scales % 16 == 0 &&
                      (uintptr_t)a.A.scales % 16 == 0 && (uintptr_t)a.B.scales % 16 == 0;
@@ -21,7 +21,7 @@ bool linear256_layout_ok(const GatedArgs& a) {
          slots * ((a.N + 255) / 256) < lim;
 }
 
-hipError_t launch_linear256(const GatedArgs& a, hipStream_t st) {
+hipError_t launch_linear256(const LinearArgs& a, hipStream_t st) {
   if (a.act != 3) return launch_linear256_act(a, st);
   constexpr int OUT = t256::OUT_LINEAR + 3;
   if (a.a_2d) return a.b_2d ? launch_out<true, true, OUT>(a, st) : launch_out<true, false, OUT>(a, st);

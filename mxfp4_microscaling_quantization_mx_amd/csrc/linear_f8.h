@@ -61,7 +61,7 @@ __global__ __launch_bounds__(512, 1) void k_grouped_linear_f8(MxOperand A, MxOpe
 }
 
 template <int FA, int FB, int OUT>
-hipError_t launch_f8(const GatedArgs& a, hipStream_t st) {
+hipError_t launch_f8(const LinearArgs& a, hipStream_t st) {
   const int cus = cu_count();
   const int tiles_n = (int)((a.N + 255) / 256);
   const int64_t tiles_m = a.offsets ? (a.M + 255) / 256 + a.E : (a.M + 255) / 256;
@@ -78,7 +78,7 @@ hipError_t launch_f8(const GatedArgs& a, hipStream_t st) {
 }
 
 template <int FA, int OUT>
-hipError_t launch_f8_b(const GatedArgs& a, hipStream_t st) {
+hipError_t launch_f8_b(const LinearArgs& a, hipStream_t st) {
   switch (a.b_elem) {
     case 1: return launch_f8<FA, 1, OUT>(a, st);
     case 2: return launch_f8<FA, 2, OUT>(a, st);

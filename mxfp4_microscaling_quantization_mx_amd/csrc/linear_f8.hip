@@ -6,7 +6,7 @@ namespace mx {
 
 // Scale rows are fetched a 32-bit word at a time; 256 rows of the operands and of
 // the buffers are addressed with 32-bit offsets.
-bool linear_f8_layout_ok(const GatedArgs& a) {
+bool linear_f8_layout_ok(const LinearArgs& a) {
   const int64_t lim = 1ll << 31;
   const bool words = a.A.ld_scales % 4 == 0 && a.B.ld_scales % 4 == 0 && a.stride_scales % 4 == 0 &&
                      (uintptr_t)a.A.scales % 4 == 0 && (uintptr_t)a.B.scales % 4 == 0;
@@ -18,7 +18,7 @@ bool linear_f8_layout_ok(const GatedArgs& a) {
          slots * ((a.N + 255) / 256) < lim;
 }
 
-hipError_t launch_linear_f8(const GatedArgs& a, hipStream_t st) {
+hipError_t launch_linear_f8(const LinearArgs& a, hipStream_t st) {
   if (a.backward) return launch_linear_f8_backward(a, st);
   switch (a.a_elem) {
     case 1: return launch_f8_b<1, 4>(a, st);

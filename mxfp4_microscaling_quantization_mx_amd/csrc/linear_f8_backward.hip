@@ -3,7 +3,7 @@
 
 namespace mx {
 
-hipError_t launch_linear_f8_backward(const GatedArgs& a, hipStream_t st) {
+hipError_t launch_linear_f8_backward(const LinearArgs& a, hipStream_t st) {
   switch (a.a_elem) {
     case 1: return launch_f8_b<1, 5>(a, st);
     case 2: return launch_f8_b<2, 5>(a, st);

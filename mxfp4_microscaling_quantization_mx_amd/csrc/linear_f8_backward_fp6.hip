@@ -3,7 +3,7 @@
 
 namespace mx {
 
-hipError_t launch_linear_f8_backward_fp6(const GatedArgs& a, hipStream_t st) {
+hipError_t launch_linear_f8_backward_fp6(const LinearArgs& a, hipStream_t st) {
   return a.a_elem == 3 ? launch_f8_b<3, 5>(a, st) : launch_f8_b<4, 5>(a, st);
 }
 

@@ -1201,7 +1201,7 @@ struct Buffer {
 // residual (p null: none) or, backward, dY.
 mx_status linear_args(const mx_tensor* A, const mx_tensor* B, const mx_epilogue_cfg* cfg, const void* bias,
                       int32_t bias_dtype, int64_t bias_stride, bool backward, const Buffer& r, const Buffer& out,
-                      const char* what, mx::GatedArgs& a) {
+                      const char* what, mx::LinearArgs& a) {
   char name[64];
   std::snprintf(name, sizeof(name), "%s: A", what);
   mx_status st = check_tensor(A, name);
@@ -1224,7 +1224,7 @@ mx_status linear_args(const mx_tensor* A, const mx_tensor* B, const mx_epilogue_
     return fail(MX_ERR_INVALID_ARG, "%s: unknown %s dtype %d", what, backward ? "dY" : "residual", r.dtype);
   if (A->rows > 0x7FFFFFFF || B->rows > 0x7FFFFFFF || A->K > 0x7FFFFFFF)
     return fail(MX_ERR_UNSUPPORTED, "%s: at most 2^31 - 1 rows and K elements", what);
-  a = mx::GatedArgs{};
+  a = mx::LinearArgs{};
   a.A = operand(A);
   a.B = operand(B);
   a.a_2d = A->block == MX_BLOCK_2D;
@@ -1262,7 +1262,7 @@ mx_status mx_linear(const mx_tensor* A, const mx_tensor* B, const mx_epilogue_cf
                     int64_t ldy, void* stream) {
   g_err[0] = '\0';
   const char* what = "mx_linear";
-  mx::GatedArgs a;
+  mx::LinearArgs a;
   mx_status st = linear_args(A, B, cfg, bias, bias_dtype, 0, false, {residual, r_dtype, ldr}, {Y, y_dtype, ldy}, what, a);
   if (st != MX_OK) return st;
   return hip_status(mx::launch_linear(a, static_cast<hipStream_t>(stream)), what);
@@ -1273,7 +1273,7 @@ mx_status mx_linear_backward(const mx_tensor* A, const mx_tensor* B, const mx_ep
                              int32_t dp_dtype, int64_t lddp, void* stream) {
   g_err[0] = '\0';
   const char* what = "mx_linear_backward";
-  mx::GatedArgs a;
+  mx::LinearArgs a;
   mx_status st = linear_args(A, B, cfg, bias, bias_dtype, 0, true, {dY, dy_dtype, lddy}, {dP, dp_dtype, lddp}, what, a);
   if (st != MX_OK) return st;
   return hip_status(mx::launch_linear(a, static_cast<hipStream_t>(stream)), what);
@@ -1285,7 +1285,7 @@ mx_status mx_grouped_linear(const mx_tensor* A, const int32_t* d_group_offsets, 
                             int32_t r_dtype, int64_t ldr, void* Y, int32_t y_dtype, int64_t ldy, void* stream) {
   g_err[0] = '\0';
   const char* what = "mx_grouped_linear";
-  mx::GatedArgs a;
+  mx::LinearArgs a;
   mx_status st = linear_args(A, B, cfg, bias, bias_dtype, bias_stride, false, {residual, r_dtype, ldr},
                              {Y, y_dtype, ldy}, what, a);
   if (st == MX_OK) st = gated_groups(a, A, d_group_offsets, E, expert_stride_codes, expert_stride_scales, what);
@@ -1300,7 +1300,7 @@ mx_status mx_grouped_linear_backward(const mx_tensor* A, const int32_t* d_group_
                                      int32_t dp_dtype, int64_t lddp, void* stream) {
   g_err[0] = '\0';
   const char* what = "mx_grouped_linear_backward";
-  mx::GatedArgs a;
+  mx::LinearArgs a;
   mx_status st = linear_args(A, B, cfg, bias, bias_dtype, bias_stride, true, {dY, dy_dtype, lddy}, {dP, dp_dtype, lddp},
                              what, a);
   if (st == MX_OK) st = gated_groups(a, A, d_group_offsets, E, expert_stride_codes, expert_stride_scales, what);

@@ -229,8 +229,12 @@ struct GatedArgs {
   const int32_t* offsets = nullptr;   // device, E+1
   int32_t E = 0;
   int64_t stride_codes = 0, stride_scales = 0;
-  // the linear layer (N counts the weight's rows): dH is the residual (null: none)
-  // or, with backward, dY; act 3 is none
+};
+
+// The linear layer (N counts the weight's rows): dH is the residual (null: none) or, with
+// backward, dY; act 3 is none.  (Apart from the gated block's, whose kernels take their
+// arguments as they are.)
+struct LinearArgs : GatedArgs {
   bool backward = false;
   const void* bias = nullptr;         // [N], grouped [E, N] with row stride bias_stride
   bool bias_bf16 = false;
@@ -321,14 +325,14 @@ hipError_t launch_gated256(const GatedArgs& a, hipStream_t st);
 bool gated_f8_layout_ok(const GatedArgs& a);
 hipError_t launch_gated_f8(const GatedArgs& a, hipStream_t st);
 // The linear layer with its epilogue, on the same kernels and pipelines.
-hipError_t launch_linear(const GatedArgs& a, hipStream_t st);
-bool linear256_layout_ok(const GatedArgs& a);
-hipError_t launch_linear256(const GatedArgs& a, hipStream_t st);
-hipError_t launch_linear256_act(const GatedArgs& a, hipStream_t st);
-bool linear_f8_layout_ok(const GatedArgs& a);
-hipError_t launch_linear_f8(const GatedArgs& a, hipStream_t st);
-hipError_t launch_linear_f8_fp6(const GatedArgs& a, hipStream_t st);
-hipError_t launch_linear_f8_backward(const GatedArgs& a, hipStream_t st);
-hipError_t launch_linear_f8_backward_fp6(const GatedArgs& a, hipStream_t st);
+hipError_t launch_linear(const LinearArgs& a, hipStream_t st);
+bool linear256_layout_ok(const LinearArgs& a);
+hipError_t launch_linear256(const LinearArgs& a, hipStream_t st);
+hipError_t launch_linear256_act(const LinearArgs& a, hipStream_t st);
+bool linear_f8_layout_ok(const LinearArgs& a);
+hipError_t launch_linear_f8(const LinearArgs& a, hipStream_t st);
+hipError_t launch_linear_f8_fp6(const LinearArgs& a, hipStream_t st);
+hipError_t launch_linear_f8_backward(const LinearArgs& a, hipStream_t st);
+hipError_t launch_linear_f8_backward_fp6(const LinearArgs& a, hipStream_t st);
 
 }  // namespace mx

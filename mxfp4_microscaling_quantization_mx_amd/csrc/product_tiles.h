@@ -75,13 +75,13 @@ __device__ __forceinline__ float linear_value(const GateP& p, bool backward, flo
   else if (backward) return gate_act<ACT, true>(p, x, d), r * d;
   else return gate_act<ACT, false>(p, x, d) + r;
 }
-__device__ __forceinline__ float linear_out(const GatedArgs& a, const GateP& p, float x, float r) {
+__device__ __forceinline__ float linear_out(const LinearArgs& a, const GateP& p, float x, float r) {
   if (p.act == 0) return linear_value<0>(p, a.backward, x, r);
   if (p.act == 1) return linear_value<1>(p, a.backward, x, r);
   if (p.act == 2) return linear_value<2>(p, a.backward, x, r);
   return linear_value<3>(p, a.backward, x, r);
 }
-__device__ __forceinline__ float linear_bias(const GatedArgs& a, int ex, int64_t c) {
+__device__ __forceinline__ float linear_bias(const LinearArgs& a, int ex, int64_t c) {
   return a.bias ? load_out(a.bias, a.bias_bf16, ex * a.bias_stride + c) : 0.0f;
 }
 
@@ -121,7 +121,7 @@ __device__ __forceinline__ void finish16(const GatedArgs& a, const GateP& p, int
 // choice between them (a type chosen per element makes 32 waits: 34 us for 25 at 1037 x
 // 1451 x 2912).
 template <int ACT>
-__device__ __forceinline__ void finish_linear(const GatedArgs& a, const GateP& p, int64_t row0, int at, int rows,
+__device__ __forceinline__ void finish_linear(const LinearArgs& a, const GateP& p, int64_t row0, int at, int rows,
                                               uint32_t c, int ex, int hi, const v16f x[2]) {
   auto rsrc = [&](const void* base, int64_t ld, int es) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(base)) + row0 * ld * es, 0,
@@ -306,11 +306,10 @@ __device__ __forceinline__ void tile_read(uint32_t row, int key, int hi, int ste
   }
 }
 
-template <bool LIN, int FA, int FB>
-__device__ __forceinline__ void row_tiles(const GatedArgs& a, const GateP& p, int64_t tiles, int64_t tiles_n, int a_words,
+template <bool LIN, int FA, int FB, class Args>
+__device__ __forceinline__ void row_tiles(const Args& a, const GateP& p, int64_t tiles, int64_t tiles_n, int a_words,
                                           int b_words) {
   constexpr int TN = LIN ? 128 : 64;                  // columns
-  const int64_t nb = weight_rows<LIN>(a);
   using OA = TileOp<FA>;
   using OB = TileOp<FB>;
   using SL = TileSlot<FA, FB>;
@@ -333,15 +332,18 @@ __device__ __forceinline__ void row_tiles(const GatedArgs& a, const GateP& p, in
     // rows and columns past the end read the last one; their results are dropped
     auto a_row = [&](int r) { return r < rows ? r : rows - 1; };
     auto b_row = [&](int r) {
-      if constexpr (LIN) return n0 + r < a.N ? n0 + r : (int)a.N - 1;
-      const int c = n0 + 32 * (r >> 6) + (r & 31), n = c < a.N ? c : (int)a.N - 1, up = (r >> 5) & 1;
-      return a.halves ? up * (int)a.N + n : 2 * n + up;
+      if constexpr (LIN) {
+        return n0 + r < a.N ? n0 + r : (int)a.N - 1;
+      } else {
+        const int c = n0 + 32 * (r >> 6) + (r & 31), n = c < a.N ? c : (int)a.N - 1, up = (r >> 5) & 1;
+        return a.halves ? up * (int)a.N + n : 2 * n + up;
+      }
     };
     TileLoads<FA> la;
     TileLoads<FB> lb;
     la.r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.A.codes + row0 * a.A.ld_codes), 0,
                                              (uint32_t)(rows * a.A.ld_codes), 0x00020000);
-    lb.r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(bc), 0, (uint32_t)(nb * a.B.ld_codes),
+    lb.r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(bc), 0, (uint32_t)(weight_rows<LIN>(a) * a.B.ld_codes),
                                              0x00020000);
 #pragma unroll
     for (int i = 0; i < OA::LOADS; ++i) {
@@ -361,8 +363,8 @@ __device__ __forceinline__ void row_tiles(const GatedArgs& a, const GateP& p, in
     const int64_t s0 = sa ? row0 : 0;                 // (A's rows count from row0)
     const bool s2 = sa ? a.a_2d : a.b_2d;
     const int64_t sld = sa ? a.A.ld_scales : a.B.ld_scales;
-    const int64_t sfirst = s2 ? s0 >> 5 : s0, slast = s2 ? (s0 + (sa ? rows : nb) - 1) >> 5
-                                                         : s0 + (sa ? rows : nb) - 1;
+    const int64_t sfirst = s2 ? s0 >> 5 : s0, slast = s2 ? (s0 + (sa ? rows : weight_rows<LIN>(a)) - 1) >> 5
+                                                         : s0 + (sa ? rows : weight_rows<LIN>(a)) - 1;
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint8_t*>((sa ? a.A.scales : bs) + sfirst * sld), 0, (uint32_t)((slast - sfirst + 1) * sld),
         0x00020000);

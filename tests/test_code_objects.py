@@ -51,3 +51,12 @@ def test_output_buffers_are_uniform(objects, family, tmp_path):
             count = sum(m.startswith("v_readfirstlane") for m in code)
             stores = sum(m.startswith("buffer_store") for m in code)
             assert stores and count < 150, (name, count, stores)
+
+
+def test_the_gated_block_takes_its_own_arguments(objects):
+    """Kernels that share a body do not share the linear layer's arguments (with them the gated
+    block's 128-row tiles took 1-3 % longer)."""
+    size = {n: k[".kernarg_segment_size"] for _, ks in objects for n, k in ks.items()}
+    linear = {size[n] for n in of_family("k_linear_tile", size)}
+    gated = {size[n] for f in ("k_gated_tile", "k_gated_few") for n in of_family(f, size)}
+    assert linear and gated and max(gated) < min(linear)
